@@ -48,8 +48,9 @@ struct Slabs {
 // element range (the next bucket of the same step).  wait_first = true
 // launches it as a programmatic dependent of whatever kernel precedes it,
 // on whose results it may depend: its CTAs may become resident while that
-// kernel finishes, but touch no memory before it has completed (the first
-// bucket of a step, after the previous step's last bucket).
+// kernel finishes, but touch no memory, nor let a dependent launch, before it
+// has completed (the first bucket of a step, after the previous step's last
+// bucket).
 cudaError_t launch_fused(const Slabs &s, const AdamScalars &c, size_t begin,
                          size_t end, int max_ctas, bool chain,
                          cudaStream_t stream, bool wait_first = false);

@@ -23,13 +23,14 @@
 //     lock step).  The loop is still grid-stride so a CTA budget can cap it;
 //   * consecutive buckets of one call are chained with programmatic
 //     dependent launch: each block lets the next bucket's grid launch as
-//     soon as it starts, and waits for the previous bucket's grid to finish
+//     soon as its own work starts, and waits for the previous bucket's grid to finish
 //     only when its own work is done.  Buckets touch disjoint elements, so
 //     the next bucket's blocks fill SMs as this bucket's tail drains, and
 //     the final wait keeps completion transitive (the last bucket of a call
 //     completes only after every earlier one).  A step's first bucket (and
 //     a rank step) is a programmatic dependent too, but waits before it
-//     touches memory, since it may read what the previous kernel wrote;
+//     touches memory, since it may read what the previous kernel wrote, and
+//     lets the next bucket launch only after that wait;
 //   * under a CTA budget the same per-vector code runs in wide CTAs (768
 //     threads, one per SM, grid = the budget, each thread striding over the
 //     range), with the fp32 state in 32-byte accesses where it is 32-byte
@@ -328,8 +329,11 @@ __device__ __forceinline__ void wait_for_predecessor_grid() {
 template <int R, bool ACC, bool ONE_OUT, bool FAST, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == kThreads ? CC_DP_MIN_BLOCKS : 1)
 fused_step_kernel(const __grid_constant__ FusedParams p) {
-    allow_dependents_to_launch();
+    // A bucket that waits first lets the next one launch only then: the next one
+    // does not wait before its work, so nothing else keeps it behind a predecessor
+    // of this call that lets its own dependents start early.
     if (p.wait_first) wait_for_predecessor_grid();
+    allow_dependents_to_launch();
     const size_t stride = static_cast<size_t>(gridDim.x) * THREADS;
     const size_t first = static_cast<size_t>(blockIdx.x) * THREADS + threadIdx.x;
     if constexpr (threads_per_vector<ACC>() == 2) {

@@ -148,6 +148,7 @@ _SIGNATURES = {
     "cc_fused_dp_muon": ([_vp, _vp, _vp, _vp, _vp, _sz, _i, _vp, _i, _i, _i, _f, _f, _i, _f, _f,
                           _vp, _i, _f, _f, _vp, _sz, _vp], _i),
     "cc_inject_bulk_stall": ([ctypes.c_longlong, ctypes.c_uint], _i),
+    "cc_inject_layernorm_stall": ([ctypes.c_longlong, ctypes.c_uint], _i),
     "cc_inject_launch_failure": ([_i], _i),
     "cc_tp_overlap_bench": ([ctypes.POINTER(cc_tp_cfg), ctypes.POINTER(cc_tp_result)], _i),
 }
@@ -709,6 +710,12 @@ def cc_inject_bulk_stall(tile: int, timeout_us: int = 20000) -> None:
     """Arm (or with -1 disarm) a one-shot skipped tile in the next bulk-engine
     launch on this thread, with its pipeline waits bounded by timeout_us."""
     _check(lib().cc_inject_bulk_stall(tile, timeout_us), "cc_inject_bulk_stall")
+
+
+def cc_inject_layernorm_stall(row: int, timeout_us: int = 20000) -> None:
+    """Skip the copies of row `row` (-1 disarms) in this thread's next layer
+    norm backward launch, with its waits bounded by timeout_us."""
+    _check(lib().cc_inject_layernorm_stall(row, timeout_us), "cc_inject_layernorm_stall")
 
 
 def cc_l2_flush(buf, nbytes: int, stream=None) -> None:

@@ -701,6 +701,15 @@ int cc_inject_bulk_stall(long long tile, unsigned timeout_us) {
     return CC_OK;
 }
 
+int cc_inject_layernorm_stall(long long row, unsigned timeout_us) {
+    if (row < -1 || row > 0x7FFFFFFFll)
+        return fail(CC_ERR_INVALID, "row=%lld must be in -1..2^31-1", row);
+    if (row >= 0 && (timeout_us < 1 || timeout_us > 1000000))
+        return fail(CC_ERR_INVALID, "timeout_us=%u must be in 1..1000000", timeout_us);
+    arm_layernorm_stall(row, 1000ull * timeout_us);
+    return CC_OK;
+}
+
 int cc_device_status(unsigned *status, int clear) {
     if (!status) return fail(CC_ERR_INVALID, "status is NULL");
     int st = ensure_device();

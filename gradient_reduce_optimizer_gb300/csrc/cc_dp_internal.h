@@ -120,6 +120,11 @@ cudaError_t read_muon_status(unsigned *status, bool clear);
 // (a wait for a row's copies ran out).  Synchronous.
 cudaError_t read_ln_status(unsigned *status, bool clear);
 
+// Arm (row >= 0) a one-shot stall of this thread's next layer norm backward
+// launch of the vector kernels: the copies of the rows that come with `row` are
+// never issued, and the launch's waits give up after limit_ns.  row < 0 disarms.
+void arm_layernorm_stall(long long row, unsigned long long limit_ns);
+
 // Multiprocessor count of the current device (queried once per device).
 cudaError_t device_sm_count(int *count);
 

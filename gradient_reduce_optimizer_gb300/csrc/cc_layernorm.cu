@@ -200,8 +200,10 @@ __device__ __forceinline__ float2 block_sum2(float a, float b, float *buf) {
 
 // The two sums over a group of warps that share a row: half the lanes carry on
 // with each, so five exchanges do for both; buf is the group's, for this row.
-__device__ __forceinline__ float2 group_sum2(float a, float b, float2 *buf, int group,
-                                             int warps) {
+// `go`, the same on a warp's lanes, becomes false on all of the group's warps if
+// it is on one; quit: the group's flag for this row, 0 until a warp sets it.
+__device__ __forceinline__ float2 group_sum2(float a, float b, float2 *buf, int group, int warps,
+                                             volatile int *quit, bool &go) {
     const int lane = threadIdx.x & 31;
     float keep = lane & 16 ? b : a;
     keep += __shfl_xor_sync(kAll, lane & 16 ? a : b, 16);
@@ -211,7 +213,9 @@ __device__ __forceinline__ float2 group_sum2(float a, float b, float2 *buf, int 
     b = __shfl_sync(kAll, keep, 16);
     if (warps == 1) return make_float2(a, b);
     if (lane == 0) buf[threadIdx.x / 32 % warps] = make_float2(a, b);
+    if (!go) *quit = 1;
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * warps) : "memory");
+    go = *quit == 0;
     const float2 v = lane < warps ? buf[lane] : make_float2(0.0f, 0.0f);
     a = warp_sum(v.x);
     b = warp_sum(v.y);
@@ -520,7 +524,14 @@ struct BwdArgs {
     int param_dtype;
     size_t rows, cols, lddy, ldx, ldds, lddx;
     float inv_cols;
+    uint32_t skip;                // the row whose fill never comes (failure injection),
+    unsigned long long limit_ns;  // or kNoRow; how long a wait lasts
 };
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+
+// What a CTA that gave up leaves in place of its partial column sums, so that
+// none are made from them: a signalling NaN, which no sum is.
+constexpr uint32_t kUnfinished = 0x7FA05EADu;
 
 // ---- rows on their way ------------------------------------------------------
 //
@@ -605,6 +616,7 @@ ln_bwd_kernel(const __grid_constant__ BwdArgs<T> p, int warps, int stages) {
     constexpr int V = kV<T>, H = V / 2;
     __shared__ __align__(8) uint64_t full[kMostStages], empty[kMostStages];
     __shared__ float2 sums[2][32];
+    __shared__ int quit[2][32];           // by turns, as the sums
     const int threads = static_cast<int>(blockDim.x);
     const int groups = threads / (32 * warps);
     const int group = static_cast<int>(threadIdx.x) / (32 * warps);
@@ -631,6 +643,7 @@ ln_bwd_kernel(const __grid_constant__ BwdArgs<T> p, int warps, int stages) {
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (threadIdx.x < 64) quit[threadIdx.x / 32][threadIdx.x % 32] = 0;
     __syncthreads();
     pdl_wait();
 
@@ -648,6 +661,7 @@ ln_bwd_kernel(const __grid_constant__ BwdArgs<T> p, int warps, int stages) {
     };
     uint32_t fills = 0;                               // bit q: stage q's copies, modulo 2
     auto fill = [&](int q, uint32_t first) {
+        if (p.skip - first < static_cast<uint32_t>(groups)) return;
         fills ^= 1u << q;
         const uint32_t n = min(static_cast<uint32_t>(groups), rows - first);
         const uint32_t bar = smem_u32(&full[q]), at = smem_u32(smem) + q * stage_bytes;
@@ -754,13 +768,15 @@ ln_bwd_kernel(const __grid_constant__ BwdArgs<T> p, int warps, int stages) {
             }
         }
     };
-    bool failed = false;
-    // A bounded wait; after one that ran out, this thread waits for nothing more.
+    // A bounded wait of a warp.  After one that ran out the warp, and with it the
+    // others that share its rows, waits for nothing more and leaves: no dx from a
+    // stage that was not filled, and no column sums of this CTA.
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (failed || mbar_wait(smem_u32(bar), parity)) return;
-        failed = true;
-        atomicOr(&g_ln_status, kStatusRows);
+        const bool there = mbar_wait(smem_u32(bar), parity, p.limit_ns);
+        if (!there) atomicOr(&g_ln_status, kStatusRows);
+        return __all_sync(kAll, there) != 0;
     };
+    bool go = true;
     int turn = 0, stage = 0, before = 0;              // before: the stage before this one
     uint32_t parity = 0, parity_before = 0;
     for (bool later = false; first < rows; first += step, later = true, turn ^= 1) {
@@ -774,10 +790,10 @@ ln_bwd_kernel(const __grid_constant__ BwdArgs<T> p, int warps, int stages) {
         // The stage before this one is filled anew as soon as every warp has
         // read it, most likely by now.
         if (filler && later && stages > 1 && first + (stages - 1) * step < rows) {
-            wait(&empty[before], parity_before);
-            if (!__any_sync(kAll, failed)) fill(before, first + (stages - 1) * step);
+            go = wait(&empty[before], parity_before);
+            if (go) fill(before, first + (stages - 1) * step);
         }
-        wait(&full[stage], parity);
+        go = go && wait(&full[stage], parity);
         const unsigned char *in = smem + stage * stage_bytes + start / 16 * 16;
         if (row < rows) {
         f2 h[HOLD ? NV : 1][H], t[HOLD ? NV : 1][H];
@@ -798,7 +814,9 @@ ln_bwd_kernel(const __grid_constant__ BwdArgs<T> p, int warps, int stages) {
             }
         }
         const float2 a = both(s1), b = both(s2);
-        const float2 s = group_sum2(a.x + a.y, b.x + b.y, sums[turn] + group * warps, group, warps);
+        const float2 s = group_sum2(a.x + a.y, b.x + b.y, sums[turn] + group * warps, group, warps,
+                                    &quit[turn][group], go);
+        if (!go) break;
         const float r1 = -rstd * (s.x * p.inv_cols), r2 = -rstd * (s.y * p.inv_cols);
         const f2 r1s = pair(r1, r1), r2s = pair(r2, r2);
         T *dx = p.dx + row * p.lddx;
@@ -834,11 +852,12 @@ ln_bwd_kernel(const __grid_constant__ BwdArgs<T> p, int warps, int stages) {
             }
         }
         }
+        if (!go) break;
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&empty[stage]));
         if (filler && stages == 1 && first + step < rows) {
-            wait(&empty[0], parity);
-            if (!__any_sync(kAll, failed)) fill(0, first + step);
+            go = wait(&empty[0], parity);
+            if (go) fill(0, first + step);
         }
         before = stage;
         parity_before = parity;
@@ -847,13 +866,18 @@ ln_bwd_kernel(const __grid_constant__ BwdArgs<T> p, int warps, int stages) {
             parity ^= 1u;
         }
     }
-    if (filler && failed)                             // let the copies in flight land
+    if (filler && !go)                                // let the copies in flight land
         for (int q = 0; q < stages; ++q) mbar_wait(smem_u32(&full[q]), (fills >> q & 1u) ^ 1u);
     if (!p.partial && !p.dweight && !p.dbias) return;
     // the groups' sums in group order, dweight then dbias, in the stages' place
     float *out = p.partial + static_cast<size_t>(blockIdx.x) * 2 * p.cols;
     float *cross = reinterpret_cast<float *>(smem);
     const bool only = !p.partial;                     // these are the results already
+    if (__syncthreads_or(!go)) {
+        if (!only)
+            for (int c = threadIdx.x; c < 2 * cols; c += threads) out[c] = __uint_as_float(kUnfinished);
+        return;
+    }
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         const bool direct = groups == 1 && !only;
@@ -934,7 +958,8 @@ ln_bwd_any_kernel(const __grid_constant__ BwdArgs<T> p) {
 }
 
 // The column sums of the CTAs' partial rows, in CTA order within each of
-// kSlices interleaved slices, the slices then in order.
+// kSlices interleaved slices, the slices then in order.  Where a CTA gave up
+// nothing is written.
 constexpr int kColsPerBlock = 32;
 constexpr int kSlices = 16;
 
@@ -950,12 +975,16 @@ ln_bwd_columns_kernel(const float *partial, int count, size_t cols, void *dweigh
     void *out = which ? dbias : dweight;
     if (!out) return;
     float s = 0.0f;
+    bool whole = true;
     if (col < cols)
 #pragma unroll 8
-        for (int q = slice; q < count; q += kSlices)
-            s += partial[(static_cast<size_t>(q) * 2 + which) * cols + col];
+        for (int q = slice; q < count; q += kSlices) {
+            const float v = partial[(static_cast<size_t>(q) * 2 + which) * cols + col];
+            whole = whole && __float_as_uint(v) != kUnfinished;
+            s += v;
+        }
     sum[slice][c] = s;
-    __syncthreads();
+    if (__syncthreads_or(!whole)) return;
     if (slice == 0 && col < cols) {
 #pragma unroll
         for (int k = 1; k < kSlices; ++k) s += sum[k][c];
@@ -1133,10 +1162,21 @@ template <typename T, bool RAGGED> auto bwd_kernel(const Shape &s) {
                        : ln_bwd_kernel<T, kFull, true, RAGGED>;
 }
 
+// One-shot injected stall of this thread's next backward launch
+// (cc_inject_layernorm_stall): the row whose fill is skipped, or -1, and the
+// limit of that launch's waits.
+thread_local long long g_stall_row = -1;
+thread_local unsigned long long g_stall_ns = 0;
+
 template <typename T>
 cudaError_t launch_bwd(BwdArgs<T> a, Rows how, void *dweight, void *dbias, int dtype,
                        cudaStream_t stream) {
     const Shape s = backward_shape(a.rows, a.cols, sizeof(T), how, a.dsum ? 3 : 2);
+    if (g_stall_row >= 0 && s.kind != Shape::kAny) {
+        a.skip = static_cast<uint32_t>(g_stall_row);
+        a.limit_ns = g_stall_ns;
+        g_stall_row = -1;
+    }
     if (s.direct) {
         a.partial = nullptr;
         a.dweight = dweight;
@@ -1268,7 +1308,8 @@ int backward_typed(const void *dy, size_t lddy, const void *x, size_t ldx, const
                  static_cast<const T *>(dsum), static_cast<T *>(dx),
                  param_of(weight, param_dtype, 1.0f), mean, rstd,
                  dweight || dbias ? workspace : nullptr, nullptr, nullptr, param_dtype,
-                 rows, cols, lddy, ldx, ldds, lddx, 1.0f / static_cast<float>(cols)};
+                 rows, cols, lddy, ldx, ldds, lddx, 1.0f / static_cast<float>(cols), kNoRow,
+                 kTimeoutNs};
     Reading how(cols, sizeof(T));
     how.add(dy, lddy);
     how.add(x, ldx);
@@ -1285,6 +1326,11 @@ size_t bwd_workspace_bytes(size_t rows, size_t cols) {
 }
 
 }  // namespace
+
+void arm_layernorm_stall(long long row, unsigned long long limit_ns) {
+    g_stall_row = row;
+    g_stall_ns = limit_ns;
+}
 
 cudaError_t read_ln_status(unsigned *status, bool clear) {
     cudaError_t e = cudaMemcpyFromSymbol(status, g_ln_status, sizeof(unsigned));

@@ -47,17 +47,18 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
-// Wait for the phase of this parity to complete, at most about kTimeoutNs.
+// Wait for the phase of this parity to complete, at most about limit_ns.
 // The timer is read once every 256 tries, so a wait that succeeds soon
 // costs only the tries.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
+                                          unsigned long long limit_ns = kTimeoutNs) {
     unsigned long long t0 = 0;
     for (uint32_t tries = 1;; ++tries) {
         if (mbar_test(bar, parity)) return true;
         if ((tries & 255u) == 0) {
             const unsigned long long now = global_ns();
             if (t0 == 0) t0 = now;
-            else if (now - t0 > kTimeoutNs) return false;
+            else if (now - t0 > limit_ns) return false;
         }
     }
 }

@@ -844,7 +844,8 @@ CC_API int cc_muon_workspace(int count, int rows, int cols, size_t *bytes);
  * 1 consumer, 2 producer, 4 drain of copies in flight.  Fused tensor-parallel
  * kernel (two seconds): 8 producer, 16 MMA, 32 epilogue, 64 drain.  The
  * orthogonalisation's products (two seconds): 256 producer, 512 MMA, 1024
- * epilogue, 2048 drain.  Layer norm (two seconds): 4096, a row's copies.  Builds
+ * epilogue, 2048 drain.  Layer norm (two seconds): 4096, a row's copies (dx of
+ * rows not reached, dweight and dbias are then left as they were).  Builds
  * with CC_DEBUG_BOUNDS=1 only: 128, an access of either kernel fell outside
  * the buffer or range its arguments describe and was skipped.  A non-zero
  * word means some launch did not finish its range.  Synchronises with the
@@ -881,6 +882,18 @@ CC_API int cc_inject_launch_failure(int after_launches);
  * cc_device_status reports the codes.  tile = -1 disarms.
  */
 CC_API int cc_inject_bulk_stall(long long tile, unsigned timeout_us);
+
+/*
+ * cc_inject_layernorm_stall -- the same for the layer norm backward pass's
+ * waits.  Arms a one-shot for the calling thread: in its next
+ * cc_layernorm_backward call (of at most 16384 columns, in vectors or
+ * contiguous) the rows that come in one copy with row `row` are never copied,
+ * and that launch's waits give up after timeout_us (1..1000000) instead of two
+ * seconds.  The CTA that waits for them leaves: its dx from those rows on, and
+ * all of dweight and dbias, keep their contents, and cc_device_status reports
+ * code 4096.  row = -1 disarms.
+ */
+CC_API int cc_inject_layernorm_stall(long long row, unsigned timeout_us);
 
 /*
  * cc_l2_flush -- overwrite `bytes` of the caller's device buffer `buf`

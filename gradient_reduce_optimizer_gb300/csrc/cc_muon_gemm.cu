@@ -668,7 +668,9 @@ __device__ __forceinline__ bool pieces_there(const Params &p, const Tile &t, int
             p.split_done + t.b,
             static_cast<unsigned>(p.cut_p.pieces > 1 ? 2 * t.k + t.kind + 1 : t.k + 1) *
                 p.split_counts);
-    return __all_sync(0xFFFFFFFFu, there) != 0;
+    there = __all_sync(0xFFFFFFFFu, there) != 0;
+    __syncwarp();                        // orders the other lanes' reads behind lane 0's acquire
+    return there;
 }
 __device__ __forceinline__ void add_sums(uint32_t (&raw)[2][32], const float *from) {
 #pragma unroll

@@ -1122,6 +1122,9 @@ ns_kernel(const __grid_constant__ Params p, const __grid_constant__ FINAL final_
             auto inside = [&](int u) { return u < units && row0 < m && t.n0 + 64 * u < n; };
             auto load = [&](int u) {
                 if (t.kind != kGram && !sums && inside(u) && elect_one()) {
+                    // what the counter announced, before this thread's copies through
+                    // the async proxy (once a tile)
+                    if (u < 2) asm volatile("fence.proxy.async.global;" ::: "memory");
                     const uint32_t bar = smem_u32(&in_full[e]);
                     const int col0 = t.n0 + 64 * u;
                     mbar_arrive_expect_tx(bar, kBox + (lo16 ? kBox : lo ? kBox / 2 : 0));
@@ -1132,7 +1135,6 @@ ns_kernel(const __grid_constant__ Params p, const __grid_constant__ FINAL final_
             };
             ok = boxes_free();
             if (ok) {
-                if (lane == 0) asm volatile("fence.proxy.async.global;" ::: "memory");
                 load(e / 4);
                 ok = __all_sync(0xFFFFFFFFu,
                                 long_wait(smem_u32(&acc_full[acc]), (n_tile >> 1) & 1));

@@ -21,7 +21,8 @@
 // Everything is computed in fp32 whatever the types in memory, and each
 // result is rounded once.  HBM bytes bound the large sizes (each activation
 // tensor moves once); launches bound the small ones, so every kernel's launch
-// overlaps the end of the one before it (griddepcontrol).
+// overlaps the end of the one before it (griddepcontrol).  That one may still be
+// writing what this one reads, so no load takes the read-only path.
 //
 // Rows in whole 16-byte vectors take ln_fwd_kernel and ln_bwd_kernel, others
 // ln_fwd_scalar_kernel and ln_bwd_kernel's RAGGED form, and rows that are wide or
@@ -65,7 +66,7 @@ template <> struct Pack<float> {
         f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
     }
     __device__ void put(const float (&f)[4]) { q = make_float4(f[0], f[1], f[2], f[3]); }
-    __device__ void load(const float *p) { q = __ldg(reinterpret_cast<const float4 *>(p)); }
+    __device__ void load(const float *p) { q = *reinterpret_cast<const float4 *>(p); }
     // vector v of a row in shared memory
     __device__ void take(const unsigned char *row, int v) {
         q = reinterpret_cast<const float4 *>(row)[v];
@@ -103,7 +104,7 @@ template <typename T> struct Pack16 {
         q = make_uint4(pack2(f[0], f[1], T{}), pack2(f[2], f[3], T{}), pack2(f[4], f[5], T{}),
                        pack2(f[6], f[7], T{}));
     }
-    __device__ void load(const T *p) { q = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ void load(const T *p) { q = *reinterpret_cast<const uint4 *>(p); }
     __device__ void take(const unsigned char *row, int v) {
         q = reinterpret_cast<const uint4 *>(row)[v];
     }
@@ -131,9 +132,9 @@ struct Param {
     float fill;
     __device__ __forceinline__ float at(size_t i) const {
         if (!p) return fill;
-        if (dtype == CC_DTYPE_F32) return __ldg(static_cast<const float *>(p) + i);
-        if (dtype == CC_DTYPE_BF16) return to_f(__ldg(static_cast<const __nv_bfloat16 *>(p) + i));
-        return to_f(__ldg(static_cast<const __half *>(p) + i));
+        if (dtype == CC_DTYPE_F32) return static_cast<const float *>(p)[i];
+        if (dtype == CC_DTYPE_BF16) return to_f(static_cast<const __nv_bfloat16 *>(p)[i]);
+        return to_f(static_cast<const __half *>(p)[i]);
     }
     // Elements i to i + V - 1, i a multiple of V.
     template <int V> __device__ __forceinline__ void vector(size_t i, float (&f)[V]) const {
@@ -144,14 +145,14 @@ struct Param {
 #pragma unroll
             for (int e = 0; e < V; e += 4) {
                 const float4 q =
-                    __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + e));
+                    *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + e);
                 f[e] = q.x; f[e + 1] = q.y; f[e + 2] = q.z; f[e + 3] = q.w;
             }
         } else {
 #pragma unroll
             for (int e = 0; e < V; e += 4) {
-                const uint2 q = __ldg(
-                    reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i + e));
+                const uint2 q =
+                    *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i + e);
                 const float2 lo = dtype == CC_DTYPE_BF16 ? unpack2(q.x, __nv_bfloat16{})
                                                          : unpack2(q.x, __half{});
                 const float2 hi = dtype == CC_DTYPE_BF16 ? unpack2(q.y, __nv_bfloat16{})
@@ -339,9 +340,11 @@ ln_fwd_kernel(const __grid_constant__ FwdArgs<T> p) {
 // are 32 elements side by side wherever the row starts; they cost more
 // instructions than vectors, but no masks, no shifts and no edges.  (The
 // aligned vectors that a row touches, masked at its ends, were slower: 16384 x
-// 1023 bf16 with its residual took 66 us, this takes 40; of 1024, 24.)
+// 1023 bf16 with its residual took 66 us, this takes 37; of 1024, 24.)
+constexpr int kScalarMost = 640;        // of eight elements a thread: two CTAs an SM
 template <typename T, int NE, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kFwdWarps)
+__global__ void __launch_bounds__(!BLOCK ? 32 * kFwdWarps : NE == 8 ? kScalarMost : 1024,
+                                  BLOCK && NE == 8 ? 2 : 1)
 ln_fwd_scalar_kernel(const __grid_constant__ FwdArgs<T> p) {
     __shared__ float buf[BLOCK ? 128 : 1];
     const int L = BLOCK ? static_cast<int>(blockDim.x) : 32;
@@ -399,17 +402,27 @@ ln_fwd_scalar_kernel(const __grid_constant__ FwdArgs<T> p) {
         if (p.rstd) p.rstd[row] = rstd;
     }
     T *y = p.y + row * p.ldy + lane;
+    // Loads of parameters do not overtake stores of y; where a thread has many, all
+    // of them come first (bf16, us, first and in turn: 16384 x 333 11.1 and 13.2,
+    // 3001 x 8191 65 and 74; with eight a warp's lane 20000 x 61 6.8 and 6.3).
+    constexpr bool kAllFirst = BLOCK || NE > 8;
     // the parameters' types, told apart once
     auto finish = [&](auto weight, auto bias) {
 #pragma unroll
         for (int k = 0; k < NE; ++k)
-            if (lane + k * L < cols)
-                y[k * L] = from_f<T>(__fmaf_rn(f[k] * rstd, weight(k * L), bias(k * L)));
+            if (lane + k * L < cols) {
+                f[k] = __fmaf_rn(f[k] * rstd, weight(k * L), bias(k * L));
+                if (!kAllFirst) y[k * L] = from_f<T>(f[k]);
+            }
+        if (!kAllFirst) return;
+#pragma unroll
+        for (int k = 0; k < NE; ++k)
+            if (lane + k * L < cols) y[k * L] = from_f<T>(f[k]);
     };
     if (p.weight.p && p.bias.p && p.weight.dtype == CC_DTYPE_F32) {
         const float *w = static_cast<const float *>(p.weight.p) + lane;
         const float *b = static_cast<const float *>(p.bias.p) + lane;
-        finish([&](int i) { return __ldg(w + i); }, [&](int i) { return __ldg(b + i); });
+        finish([&](int i) { return w[i]; }, [&](int i) { return b[i]; });
     } else {
         finish([&](int i) { return p.weight.at(lane + i); }, [&](int i) { return p.bias.at(lane + i); });
     }
@@ -716,8 +729,8 @@ ln_bwd_kernel(const __grid_constant__ BwdArgs<T> p, int warps, int stages) {
     }
     float nmean = 0.0f, nrstd = 0.0f;
     if (first + group < rows) {
-        nmean = __ldg(p.mean + first + group);
-        nrstd = __ldg(p.rstd + first + group);
+        nmean = p.mean[first + group];
+        nrstd = p.rstd[first + group];
     }
     __syncthreads();
     pdl_launch();
@@ -784,8 +797,8 @@ ln_bwd_kernel(const __grid_constant__ BwdArgs<T> p, int warps, int stages) {
         const float rstd = nrstd;
         const f2 mean2 = pair(-nmean, -nmean), rstd2 = pair(rstd, rstd);
         if (row + step < rows) {
-            nmean = __ldg(p.mean + row + step);
-            nrstd = __ldg(p.rstd + row + step);
+            nmean = p.mean[row + step];
+            nrstd = p.rstd[row + step];
         }
         // The stage before this one is filled anew as soon as every warp has
         // read it, most likely by now.
@@ -1029,7 +1042,7 @@ Shape forward_shape(size_t rows, size_t cols, size_t elem, Rows how) {
     // a CTA cost more (bf16, us, 8 and 16 elements a thread: 16384 x 333 17.5
     // (two warps) and 12.0 (one); 2000 x 5001 29.7 and 31.6; 3001 x 8191 84 and
     // 71; 32 elements on one warp: 16384 x 1023 51, 8 on four 40).
-    else s.nv = n <= 256 ? 8 : n <= 512 ? 16 : n <= 6144 ? 8 : 16;
+    else s.nv = n <= 256 ? 8 : n <= 512 ? 16 : n <= 8 * kScalarMost ? 8 : 16;
     s.threads = threads_of(n, s.nv);
     s.warps = s.threads / 32;
     // few rows: over all SMs, rather than all a CTA's warps

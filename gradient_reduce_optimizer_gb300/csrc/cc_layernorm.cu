@@ -7,7 +7,10 @@
 //   mean = sum(s) / cols,  rstd = 1 / sqrt(sum((s - mean)^2) / cols + eps)
 //   y    = (s - mean) * rstd * weight + bias
 // The row stays in registers between the two sums, so the variance is the
-// exact two-pass form (no cancellation of E[s^2] - mean^2) at one read.
+// exact two-pass form (no cancellation of E[s^2] - mean^2) at one read.  The
+// second pass also sums s - mean, which is what the first one's roundings left:
+// it corrects the mean, the variance and y.  (In a row that is all but constant
+// rstd is up to 1/sqrt(eps), and would make much of an ulp of the mean.)
 //
 // Backward, with h = (x - mean) * rstd and t = dy * weight:
 //   dx = rstd * (t - mean(t) - h * mean(t * h)) (+ dsum)
@@ -174,12 +177,45 @@ __device__ __forceinline__ void pdl_launch() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Two fp32 values to an instruction.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 both(f2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ float add(f2 a) { return both(a).x + both(a).y; }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // ---- sums over a row --------------------------------------------------------
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
     return v;
+}
+
+__device__ __forceinline__ float2 warp_sum2(float a, float b) {
+    return make_float2(warp_sum(a), warp_sum(b));
 }
 
 // The CTA's sums of a and b, the same on every thread; `buf` holds 64 floats
@@ -224,6 +260,21 @@ __device__ __forceinline__ float2 group_sum2(float a, float b, float2 *buf, int 
 }
 
 // ---- forward ----------------------------------------------------------------
+
+// A row's statistics from its first mean m and the sums of the deviations d from
+// it and of their squares: the mean, 1 / sqrt(variance + eps), and the shift that
+// makes d * rstd + shift the normalised element.
+struct RowStats {
+    float mean, rstd, shift;
+};
+__device__ __forceinline__ RowStats row_stats(float m, float sum_d, float sum_d2, float inv_cols,
+                                              float eps) {
+    const float c = sum_d * inv_cols;
+    float var = __fmaf_rn(-c, c, sum_d2 * inv_cols);
+    if (var < 0.0f) var = 0.0f;                       // a rounding; NaN stays
+    const float rstd = __frsqrt_rn(var + eps);
+    return {m + c, rstd, -c * rstd};
+}
 
 template <typename T>
 struct FwdArgs {
@@ -302,21 +353,25 @@ ln_fwd_kernel(const __grid_constant__ FwdArgs<T> p) {
         }
     s = BLOCK ? block_sum2(s, 0.0f, buf).x : warp_sum(s);
     const float mean = s * p.inv_cols;
-    float q = 0.0f;
+    const f2 less = pair(-mean, -mean);
+    f2 c = 0, q = 0;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
         if (lane + k * L < nvec) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                f[k][e] -= mean;
-                q = __fmaf_rn(f[k][e], f[k][e], q);
+            for (int e = 0; e < V; e += 2) {
+                const f2 d = add2(pair(f[k][e], f[k][e + 1]), less);
+                c = add2(c, d);
+                q = fma2(d, d, q);
+                f[k][e] = both(d).x;
+                f[k][e + 1] = both(d).y;
             }
         }
-    q = BLOCK ? block_sum2(q, 0.0f, buf + 64).x : warp_sum(q);
-    const float rstd = __frsqrt_rn(__fmaf_rn(q, p.inv_cols, p.eps));
+    const float2 sums = BLOCK ? block_sum2(add(c), add(q), buf + 64) : warp_sum2(add(c), add(q));
+    const RowStats st = row_stats(mean, sums.x, sums.y, p.inv_cols, p.eps);
     if (lane == 0) {
-        if (p.mean) p.mean[row] = mean;
-        if (p.rstd) p.rstd[row] = rstd;
+        if (p.mean) p.mean[row] = st.mean;
+        if (p.rstd) p.rstd[row] = st.rstd;
     }
     T *y = p.y + row * p.ldy;
 #pragma unroll
@@ -327,7 +382,8 @@ ln_fwd_kernel(const __grid_constant__ FwdArgs<T> p) {
             p.weight.vector(static_cast<size_t>(v) * V, w);
             p.bias.vector(static_cast<size_t>(v) * V, b);
 #pragma unroll
-            for (int e = 0; e < V; ++e) f[k][e] = __fmaf_rn(f[k][e] * rstd, w[e], b[e]);
+            for (int e = 0; e < V; ++e)
+                f[k][e] = __fmaf_rn(__fmaf_rn(f[k][e], st.rstd, st.shift), w[e], b[e]);
             Pack<T> o;
             o.put(f[k]);
             o.store(y + static_cast<size_t>(v) * V);
@@ -340,7 +396,7 @@ ln_fwd_kernel(const __grid_constant__ FwdArgs<T> p) {
 // are 32 elements side by side wherever the row starts; they cost more
 // instructions than vectors, but no masks, no shifts and no edges.  (The
 // aligned vectors that a row touches, masked at its ends, were slower: 16384 x
-// 1023 bf16 with its residual took 66 us, this takes 37; of 1024, 24.)
+// 1023 bf16 with its residual took 66 us, this takes 39; of 1024, 24.)
 constexpr int kScalarMost = 640;        // of eight elements a thread: two CTAs an SM
 template <typename T, int NE, bool BLOCK>
 __global__ void __launch_bounds__(!BLOCK ? 32 * kFwdWarps : NE == 8 ? kScalarMost : 1024,
@@ -388,18 +444,24 @@ ln_fwd_scalar_kernel(const __grid_constant__ FwdArgs<T> p) {
     for (int k = 0; k < NE; ++k)
         if (lane + k * L < cols) s += f[k];
     const float mean = (BLOCK ? block_sum2(s, 0.0f, buf).x : warp_sum(s)) * p.inv_cols;
-    float q = 0.0f;
+    const f2 less = pair(-mean, -mean);
+    f2 c = 0, q = 0;
 #pragma unroll
-    for (int k = 0; k < NE; ++k)
-        if (lane + k * L < cols) {
-            f[k] -= mean;
-            q = __fmaf_rn(f[k], f[k], q);
-        }
-    q = BLOCK ? block_sum2(q, 0.0f, buf + 64).x : warp_sum(q);
-    const float rstd = __frsqrt_rn(__fmaf_rn(q, p.inv_cols, p.eps));
+    for (int k = 0; k < NE; k += 2) {
+        // what lies past the row deviates by nothing
+        if (lane + k * L >= cols) f[k] = mean;
+        if (lane + (k + 1) * L >= cols) f[k + 1] = mean;
+        const f2 d = add2(pair(f[k], f[k + 1]), less);
+        c = add2(c, d);
+        q = fma2(d, d, q);
+        f[k] = both(d).x;
+        f[k + 1] = both(d).y;
+    }
+    const float2 sums = BLOCK ? block_sum2(add(c), add(q), buf + 64) : warp_sum2(add(c), add(q));
+    const RowStats st = row_stats(mean, sums.x, sums.y, p.inv_cols, p.eps);
     if (lane == 0) {
-        if (p.mean) p.mean[row] = mean;
-        if (p.rstd) p.rstd[row] = rstd;
+        if (p.mean) p.mean[row] = st.mean;
+        if (p.rstd) p.rstd[row] = st.rstd;
     }
     T *y = p.y + row * p.ldy + lane;
     // Loads of parameters do not overtake stores of y; where a thread has many, all
@@ -411,13 +473,14 @@ ln_fwd_scalar_kernel(const __grid_constant__ FwdArgs<T> p) {
 #pragma unroll
         for (int k = 0; k < NE; ++k)
             if (lane + k * L < cols) {
-                f[k] = __fmaf_rn(f[k] * rstd, weight(k * L), bias(k * L));
+                f[k] = __fmaf_rn(__fmaf_rn(f[k], st.rstd, st.shift), weight(k * L), bias(k * L));
                 if (!kAllFirst) y[k * L] = from_f<T>(f[k]);
             }
-        if (!kAllFirst) return;
+        if constexpr (kAllFirst) {
 #pragma unroll
-        for (int k = 0; k < NE; ++k)
-            if (lane + k * L < cols) y[k * L] = from_f<T>(f[k]);
+            for (int k = 0; k < NE; ++k)
+                if (lane + k * L < cols) y[k * L] = from_f<T>(f[k]);
+        }
     };
     if (p.weight.p && p.bias.p && p.weight.dtype == CC_DTYPE_F32) {
         const float *w = static_cast<const float *>(p.weight.p) + lane;
@@ -446,22 +509,24 @@ ln_fwd_any_kernel(const __grid_constant__ FwdArgs<T> p) {
     float s = 0.0f;
     for (size_t i = threadIdx.x; i < p.cols; i += kScalarThreads) s += at(i);
     const float mean = block_sum2(s, 0.0f, buf).x * p.inv_cols;
-    float q = 0.0f;
+    float q = 0.0f, c = 0.0f;
     for (size_t i = threadIdx.x; i < p.cols; i += kScalarThreads) {
         const float d = at(i) - mean;
+        c += d;
         q = __fmaf_rn(d, d, q);
     }
-    const float rstd =
-        __frsqrt_rn(__fmaf_rn(block_sum2(q, 0.0f, buf + 64).x, p.inv_cols, p.eps));
+    const float2 sums = block_sum2(c, q, buf + 64);
+    const RowStats st = row_stats(mean, sums.x, sums.y, p.inv_cols, p.eps);
     if (threadIdx.x == 0) {
-        if (p.mean) p.mean[row] = mean;
-        if (p.rstd) p.rstd[row] = rstd;
+        if (p.mean) p.mean[row] = st.mean;
+        if (p.rstd) p.rstd[row] = st.rstd;
     }
     for (size_t i = threadIdx.x; i < p.cols; i += kScalarThreads) {
         const float v = at(i);
         if (p.sum_out) p.sum_out[row * p.lds + i] = from_f<T>(v);
         p.y[row * p.ldy + i] =
-            from_f<T>(__fmaf_rn((v - mean) * rstd, p.weight.at(i), p.bias.at(i)));
+            from_f<T>(__fmaf_rn(__fmaf_rn(v - mean, st.rstd, st.shift), p.weight.at(i),
+                                p.bias.at(i)));
     }
 }
 
@@ -570,34 +635,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 // Without copies in flight the next rows' latency would be exposed: while a
 // block of rows is worked on, the next `stages` - 1 are on their way.
 constexpr int kMostStages = 8;
-
-// Two fp32 values to an instruction.
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 pair(float lo, float hi) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 both(f2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 
 // Bytes of a tensor's rows in a stage (ragged ones with what they share of a
 // vector at either end).

@@ -601,7 +601,7 @@ struct BwdArgs {
     void *dweight, *dbias;        // the results (of one CTA), each null: not wanted
     int param_dtype;
     size_t rows, cols, lddy, ldx, ldds, lddx;
-    float inv_cols;
+    float cols_f, inv_cols;
     uint32_t skip;                // the row whose fill never comes (failure injection),
     unsigned long long limit_ns;  // or kNoRow; how long a wait lasts
 };
@@ -867,8 +867,10 @@ ln_bwd_kernel(const __grid_constant__ BwdArgs<T> p, int warps, int stages) {
         const float2 s = group_sum2(a.x + a.y, b.x + b.y, sums[turn] + group * warps, group, warps,
                                     &quit[turn][group], go);
         if (!go) break;
-        const float r1 = -rstd * (s.x * p.inv_cols), r2 = -rstd * (s.y * p.inv_cols);
-        const f2 r1s = pair(r1, r1), r2s = pair(r2, r2);
+        // The mean of t a quotient, not a product with 1 / cols, and taken off before rstd is
+        // multiplied: equal gradients leave nothing.
+        const float m1 = -__fdiv_rn(s.x, p.cols_f), m2 = -(s.y * p.inv_cols);
+        const f2 m1s = pair(m1, m1), m2s = pair(m2, m2);
         T *dx = p.dx + row * p.lddx;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -881,7 +883,7 @@ ln_bwd_kernel(const __grid_constant__ BwdArgs<T> p, int warps, int stages) {
                 float o[V];
 #pragma unroll
                 for (int e = 0; e < H; ++e) {
-                    const float2 d = both(fma2(t[at][e], rstd2, fma2(h[at][e], r2s, r1s)));
+                    const float2 d = both(mul2(fma2(h[at][e], m2s, add2(t[at][e], m1s)), rstd2));
                     o[2 * e] = d.x;
                     o[2 * e + 1] = d.y;
                 }
@@ -996,7 +998,7 @@ ln_bwd_any_kernel(const __grid_constant__ BwdArgs<T> p) {
             }
         }
         const float2 s = block_sum2(s1, s2, buf + 64 * which);
-        s1 = s.x * p.inv_cols;
+        s1 = __fdiv_rn(s.x, p.cols_f);
         s2 = s.y * p.inv_cols;
         for (size_t i = threadIdx.x; i < p.cols; i += kScalarThreads) {
             const float h = (to_f(x[i]) - mean) * rstd;
@@ -1358,8 +1360,8 @@ int backward_typed(const void *dy, size_t lddy, const void *x, size_t ldx, const
                  static_cast<const T *>(dsum), static_cast<T *>(dx),
                  param_of(weight, param_dtype, 1.0f), mean, rstd,
                  dweight || dbias ? workspace : nullptr, nullptr, nullptr, param_dtype,
-                 rows, cols, lddy, ldx, ldds, lddx, 1.0f / static_cast<float>(cols), kNoRow,
-                 kTimeoutNs};
+                 rows, cols, lddy, ldx, ldds, lddx, static_cast<float>(cols),
+                 1.0f / static_cast<float>(cols), kNoRow, kTimeoutNs};
     Reading how(cols, sizeof(T));
     how.add(dy, lddy);
     how.add(x, ldx);

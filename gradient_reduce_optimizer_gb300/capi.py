@@ -539,6 +539,10 @@ def _calls():
     return _CALLS
 
 
+_ITEM = {CC_DTYPE_BF16: 2, CC_DTYPE_F16: 2, CC_DTYPE_F32: 4}
+_TYPE_NAME = {CC_DTYPE_BF16: "bf16", CC_DTYPE_F16: "fp16", CC_DTYPE_F32: "fp32"}
+
+
 def _dtype(t, given: Optional[int], name: str) -> int:
     """The CC_DTYPE_* code: `given`, or that of the tensor."""
     if given is not None:
@@ -561,6 +565,27 @@ def _param_dtype(tensors, given: Optional[int], act: int, name: str) -> int:
     return act
 
 
+def _check_type(t, code: int, what: str, name: str) -> None:
+    """Refuse a tensor whose type is not the one of this code.  (Types that are
+    none of the three, such as int16 for the bits of bf16, need its width.)"""
+    _torch()
+    own = _DTYPES.get(t.dtype)
+    if code in _ITEM and (own != code if own is not None else t.element_size() != _ITEM[code]):
+        raise CCError(CC_ERR_INVALID, name, f"{what} is {t.dtype}, the call takes it as "
+                      f"{_TYPE_NAME[code]}")
+
+
+def _vector(t, code: int, count: int, what: str, name: str) -> Optional[int]:
+    """The address of `count` contiguous elements of the type of this code."""
+    if t is None or isinstance(t, int):
+        return t
+    _check_type(t, code, what, name)
+    if not t.is_contiguous() or t.numel() < count:
+        raise CCError(CC_ERR_INVALID, name, f"{what} must be {count} contiguous elements (shape "
+                      f"{tuple(t.shape)}, strides {t.stride()})")
+    return t.data_ptr()
+
+
 def _rows_stride(t, cols: int, name: str) -> int:
     """Elements between the rows of a tensor whose last dimension is the row
     (cols for a raw pointer or None): every leading dimension must step
@@ -578,11 +603,38 @@ def _rows_stride(t, cols: int, name: str) -> int:
     return dims[-1][1] if dims else cols
 
 
+def _rows(t, code: int, rows: int, cols: int, what: str, name: str) -> Tuple[Optional[int], int]:
+    """(address, elements between rows) of rows x cols elements of the type of
+    this code."""
+    if t is None or isinstance(t, int):
+        return t, cols
+    _check_type(t, code, what, name)
+    stride = _rows_stride(t, cols, name)
+    if t.is_contiguous():
+        short = t.numel() < rows * cols
+    else:
+        short = t.shape[-1] < cols or t.numel() // t.shape[-1] < rows
+    if short:
+        raise CCError(CC_ERR_INVALID, name, f"{what} of shape {tuple(t.shape)} holds no {rows} rows "
+                      f"of {cols}")
+    return t.data_ptr(), stride
+
+
+def _workspace(t, nbytes: int, name: str) -> Optional[int]:
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+        raise CCError(CC_ERR_INVALID, name, f"the workspace must be {nbytes} contiguous bytes (shape "
+                      f"{tuple(t.shape)} of {t.dtype})")
+    return t.data_ptr()
+
+
 def cc_layernorm_forward(x, weight, bias, y, mean, rstd, rows: int, cols: int, eps: float, *,
                          residual=None, sum_out=None, act_dtype: Optional[int] = None,
                          param_dtype: Optional[int] = None, stream=None) -> None:
     """Layer norm of rows x cols, with the residual addition before it.  Row
-    strides and element types come from the tensors; raw pointers are
+    strides and element types come from the tensors: x, residual, y and sum_out
+    of one type, weight and bias of one, mean and rstd fp32.  Raw pointers are
     contiguous rows and need act_dtype and param_dtype."""
     f = "cc_layernorm_forward"
     if act_dtype is None and param_dtype is None and stream is None:
@@ -593,10 +645,11 @@ def cc_layernorm_forward(x, weight, bias, y, mean, rstd, rows: int, cols: int, e
     act = _dtype(x, act_dtype, f)
     par = _param_dtype((weight, bias), param_dtype, act, f)
     _check(lib().cc_layernorm_forward(
-        _addr(x), _rows_stride(x, cols, f), _addr(residual), _rows_stride(residual, cols, f),
-        _addr(weight), _addr(bias), _addr(y), _rows_stride(y, cols, f), _addr(sum_out),
-        _rows_stride(sum_out, cols, f), _addr(mean), _addr(rstd), rows, cols, eps, act, par,
-        _stream(stream)), f)
+        *_rows(x, act, rows, cols, "x", f), *_rows(residual, act, rows, cols, "residual", f),
+        _vector(weight, par, cols, "weight", f), _vector(bias, par, cols, "bias", f),
+        *_rows(y, act, rows, cols, "y", f), *_rows(sum_out, act, rows, cols, "sum_out", f),
+        _vector(mean, CC_DTYPE_F32, rows, "mean", f), _vector(rstd, CC_DTYPE_F32, rows, "rstd", f),
+        rows, cols, eps, act, par, _stream(stream)), f)
 
 
 def cc_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, rows: int, cols: int,
@@ -604,7 +657,8 @@ def cc_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, rows: i
                           act_dtype: Optional[int] = None, param_dtype: Optional[int] = None,
                           stream=None) -> None:
     """The gradients of cc_layernorm_forward (dx, and dweight and dbias summed
-    over the rows)."""
+    over the rows); dy, x, dx and dsum of one type, weight, dweight and dbias of
+    one, mean and rstd fp32."""
     f = "cc_layernorm_backward"
     if act_dtype is None and param_dtype is None and stream is None:
         status = (_CALLS or _calls()).layernorm_backward(
@@ -615,10 +669,12 @@ def cc_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, rows: i
     act = _dtype(x, act_dtype, f)
     par = _param_dtype((weight, dweight, dbias), param_dtype, act, f)
     _check(lib().cc_layernorm_backward(
-        _addr(dy), _rows_stride(dy, cols, f), _addr(x), _rows_stride(x, cols, f), _addr(weight),
-        _addr(mean), _addr(rstd), _addr(dsum), _rows_stride(dsum, cols, f), _addr(dx),
-        _rows_stride(dx, cols, f), _addr(dweight), _addr(dbias), rows, cols, act, par,
-        _addr(workspace), workspace_bytes, _stream(stream)), f)
+        *_rows(dy, act, rows, cols, "dy", f), *_rows(x, act, rows, cols, "x", f),
+        _vector(weight, par, cols, "weight", f), _vector(mean, CC_DTYPE_F32, rows, "mean", f),
+        _vector(rstd, CC_DTYPE_F32, rows, "rstd", f), *_rows(dsum, act, rows, cols, "dsum", f),
+        *_rows(dx, act, rows, cols, "dx", f), _vector(dweight, par, cols, "dweight", f),
+        _vector(dbias, par, cols, "dbias", f), rows, cols, act, par,
+        _workspace(workspace, workspace_bytes, f), workspace_bytes, _stream(stream)), f)
 
 
 def cc_layernorm_backward_workspace(rows: int, cols: int) -> int:

@@ -3,9 +3,10 @@
  * A layer norm of a few hundred rows takes the GPU about five microseconds, and
  * the same call through ctypes takes the CPU eight to ten: two thirds of it
  * Python code that asks tensors for pointers, strides and types and converts
- * them one by one.  These functions take the usual case (contiguous tensors,
- * types and stream from torch) in about one microsecond.  Everything else they
- * leave to the binding: they return SLOW before anything was called.
+ * them one by one.  These functions take the usual case (contiguous tensors of
+ * the types that belong together, all large enough, and torch's stream) in less
+ * than two microseconds.  Everything else they leave to the binding, which takes
+ * it or says what is wrong with it: they return SLOW before anything was called.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -25,7 +26,7 @@ static forward_fn g_forward;
 static backward_fn g_backward;
 static PyObject *g_dtypes[3];              /* by CC_DTYPE_* code */
 static PyObject *g_get_device, *g_get_stream;
-static PyObject *s_data_ptr, *s_is_contiguous, *s_dtype;
+static PyObject *s_data_ptr, *s_is_contiguous, *s_dtype, *s_nbytes;
 
 /* Each of these says whether the usual case goes on; no error is left set. */
 static int no(void) {
@@ -33,20 +34,53 @@ static int no(void) {
     return 0;
 }
 
-static int pointer(PyObject *t, int rows, void **out) {
+/* A tensor's address: contiguous, of this type and of `count` elements at least. */
+static int pointer(PyObject *t, int code, size_t count, void **out) {
     *out = NULL;
     if (t == Py_None) return 1;
     if (PyLong_Check(t)) return 0;
-    if (rows) {
-        PyObject *r = PyObject_CallMethodNoArgs(t, s_is_contiguous);
-        if (!r) return no();
-        Py_DECREF(r);
-        if (r != Py_True) return 0;
-    }
-    PyObject *p = PyObject_CallMethodNoArgs(t, s_data_ptr);
-    if (!p) return no();
-    const unsigned long long v = PyLong_AsUnsignedLongLong(p);
-    Py_DECREF(p);
+    PyObject *r = PyObject_GetAttr(t, s_dtype);
+    if (!r) return no();
+    Py_DECREF(r);
+    if (r != g_dtypes[code]) return 0;
+    r = PyObject_CallMethodNoArgs(t, s_is_contiguous);
+    if (!r) return no();
+    Py_DECREF(r);
+    if (r != Py_True) return 0;
+    r = PyObject_GetAttr(t, s_nbytes);
+    if (!r) return no();
+    const size_t bytes = PyLong_AsSize_t(r);
+    Py_DECREF(r);
+    if (PyErr_Occurred()) return no();
+    if (bytes / (code == CC_DTYPE_F32 ? 4 : 2) < count) return 0;
+    r = PyObject_CallMethodNoArgs(t, s_data_ptr);
+    if (!r) return no();
+    const unsigned long long v = PyLong_AsUnsignedLongLong(r);
+    Py_DECREF(r);
+    if (PyErr_Occurred()) return no();
+    *out = (void *)(uintptr_t)v;
+    return 1;
+}
+
+/* Workspace: whatever its type, of these bytes. */
+static int workspace(PyObject *t, size_t bytes, void **out) {
+    *out = NULL;
+    if (t == Py_None) return 1;
+    if (PyLong_Check(t)) return 0;
+    PyObject *r = PyObject_GetAttr(t, s_nbytes);
+    if (!r) return no();
+    const size_t has = PyLong_AsSize_t(r);
+    Py_DECREF(r);
+    if (PyErr_Occurred()) return no();
+    if (has < bytes) return 0;
+    r = PyObject_CallMethodNoArgs(t, s_is_contiguous);
+    if (!r) return no();
+    Py_DECREF(r);
+    if (r != Py_True) return 0;
+    r = PyObject_CallMethodNoArgs(t, s_data_ptr);
+    if (!r) return no();
+    const unsigned long long v = PyLong_AsUnsignedLongLong(r);
+    Py_DECREF(r);
     if (PyErr_Occurred()) return no();
     *out = (void *)(uintptr_t)v;
     return 1;
@@ -92,16 +126,17 @@ static int stream(void **out) {
 static PyObject *layernorm_forward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
     void *x, *w, *b, *y, *mean, *rstd, *residual, *sum, *on;
-    size_t rows, cols;
+    size_t rows, cols, all;
     int act = -1, par;
-    if (!g_forward || n != 11 || a[0] == Py_None || !pointer(a[0], 1, &x) ||
-        !pointer(a[1], 0, &w) || !pointer(a[2], 0, &b) || !pointer(a[3], 1, &y) ||
-        !pointer(a[4], 0, &mean) || !pointer(a[5], 0, &rstd) || !size(a[6], &rows) ||
-        !size(a[7], &cols) || !PyFloat_Check(a[8]) || !pointer(a[9], 1, &residual) ||
-        !pointer(a[10], 1, &sum) || !dtype(a, 1, &act))
+    if (!g_forward || n != 11 || a[0] == Py_None || !size(a[6], &rows) || !size(a[7], &cols) ||
+        __builtin_mul_overflow(rows, cols, &all) || !PyFloat_Check(a[8]) || !dtype(a, 1, &act))
         return PyLong_FromLong(SLOW);
     par = act;
-    if (!dtype(a + 1, 2, &par) || !stream(&on)) return PyLong_FromLong(SLOW);
+    if (!dtype(a + 1, 2, &par) || !pointer(a[0], act, all, &x) || !pointer(a[1], par, cols, &w) ||
+        !pointer(a[2], par, cols, &b) || !pointer(a[3], act, all, &y) ||
+        !pointer(a[4], CC_DTYPE_F32, rows, &mean) || !pointer(a[5], CC_DTYPE_F32, rows, &rstd) ||
+        !pointer(a[9], act, all, &residual) || !pointer(a[10], act, all, &sum) || !stream(&on))
+        return PyLong_FromLong(SLOW);
     const float eps = (float)PyFloat_AS_DOUBLE(a[8]);
     int st;
     Py_BEGIN_ALLOW_THREADS
@@ -116,18 +151,19 @@ static PyObject *layernorm_forward(PyObject *self, PyObject *const *a, Py_ssize_
 static PyObject *layernorm_backward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
     void *dy, *x, *w, *mean, *rstd, *dx, *dw, *db, *ws, *dsum, *on;
-    size_t rows, cols, bytes;
+    size_t rows, cols, all, bytes;
     int act = -1, par;
-    if (!g_backward || n != 13 || a[1] == Py_None || !pointer(a[0], 1, &dy) ||
-        !pointer(a[1], 1, &x) || !pointer(a[2], 0, &w) || !pointer(a[3], 0, &mean) ||
-        !pointer(a[4], 0, &rstd) || !pointer(a[5], 1, &dx) || !pointer(a[6], 0, &dw) ||
-        !pointer(a[7], 0, &db) || !size(a[8], &rows) || !size(a[9], &cols) ||
-        !pointer(a[10], 0, &ws) || !size(a[11], &bytes) || !pointer(a[12], 1, &dsum) ||
-        !dtype(a + 1, 1, &act))
+    if (!g_backward || n != 13 || a[1] == Py_None || !size(a[8], &rows) || !size(a[9], &cols) ||
+        __builtin_mul_overflow(rows, cols, &all) || !size(a[11], &bytes) || !dtype(a + 1, 1, &act))
         return PyLong_FromLong(SLOW);
     par = act;
     PyObject *const params[3] = {a[2], a[6], a[7]};
-    if (!dtype(params, 3, &par) || !stream(&on)) return PyLong_FromLong(SLOW);
+    if (!dtype(params, 3, &par) || !pointer(a[0], act, all, &dy) || !pointer(a[1], act, all, &x) ||
+        !pointer(a[2], par, cols, &w) || !pointer(a[3], CC_DTYPE_F32, rows, &mean) ||
+        !pointer(a[4], CC_DTYPE_F32, rows, &rstd) || !pointer(a[5], act, all, &dx) ||
+        !pointer(a[6], par, cols, &dw) || !pointer(a[7], par, cols, &db) ||
+        !workspace(a[10], bytes, &ws) || !pointer(a[12], act, all, &dsum) || !stream(&on))
+        return PyLong_FromLong(SLOW);
     int st;
     Py_BEGIN_ALLOW_THREADS
     st = g_backward(dy, cols, x, cols, w, (const float *)mean, (const float *)rstd, dsum, cols, dx,
@@ -165,6 +201,7 @@ PyMODINIT_FUNC PyInit__calls(void) {
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
     s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
     s_dtype = PyUnicode_InternFromString("dtype");
-    if (!s_data_ptr || !s_is_contiguous || !s_dtype) return NULL;
+    s_nbytes = PyUnicode_InternFromString("nbytes");
+    if (!s_data_ptr || !s_is_contiguous || !s_dtype || !s_nbytes) return NULL;
     return PyModule_Create(&module);
 }

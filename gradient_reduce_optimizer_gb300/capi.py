@@ -734,10 +734,23 @@ def cc_muon_orthogonalise(g, out, count: int, rows: int, cols: int, workspace,
     f = "cc_muon_orthogonalise"
     ldg, sg = _matrix_strides(g, count, rows, cols, f)
     ldo, so = _matrix_strides(out, count, rows, cols, f)
+    code = _dtype(g, g_dtype, f)
+    for t, c, what in ((g, code, "g"), (out, CC_DTYPE_BF16, "out")):
+        if t is not None and not isinstance(t, int):
+            _check_type(t, c, what, f)
     _check(lib().cc_muon_orthogonalise(
-        _addr(g), ldg, sg, _addr(out), ldo, so, count, rows, cols, _dtype(g, g_dtype, f),
-        _coeffs(coeffs, steps), steps, eps, _addr(workspace), workspace_bytes, _stream(stream)),
+        _addr(g), ldg, sg, _addr(out), ldo, so, count, rows, cols, code, _coeffs(coeffs, steps),
+        steps, eps, _workspace(workspace, workspace_bytes, f), workspace_bytes, _stream(stream)),
         f)
+
+
+def _slabs(ts, code: int, n: int, R: int, what: str, name: str) -> Optional[ctypes.Array]:
+    """The addresses of R slabs of n elements of the type of this code."""
+    if ts is None:
+        return None
+    if len(ts) < R:
+        raise CCError(CC_ERR_INVALID, name, f"{what} holds {len(ts)} slabs for R={R}")
+    return _addr_array([_vector(t, code, n, f"{what}[{r}]", name) for r, t in enumerate(ts)])
 
 
 def cc_fused_dp_muon(grads, acc, master, momentum, params_out, n: int, R: int,
@@ -747,13 +760,17 @@ def cc_fused_dp_muon(grads, acc, master, momentum, params_out, n: int, R: int,
                      update_scale: float = 1.0, coeffs=MUON_COEFFS, steps: int = 5,
                      eps: float = 1e-7, grad_scale: float = 1.0, stream=None) -> None:
     """The data-parallel Muon step on the rows x cols matrices at `offsets`
-    of the slabs."""
+    of the slabs (grads and params_out bf16, the others fp32)."""
+    f = "cc_fused_dp_muon"
     count = len(offsets)
     _check(lib().cc_fused_dp_muon(
-        _addr_array(grads), _addr_array(acc), _addr(master), _addr(momentum),
-        _addr_array(params_out), n, R, (_sz * max(1, count))(*offsets), count, rows, cols, lr,
-        beta, int(bool(nesterov)), weight_decay, update_scale, _coeffs(coeffs, steps), steps, eps,
-        grad_scale, _addr(workspace), workspace_bytes, _stream(stream)), "cc_fused_dp_muon")
+        _slabs(grads, CC_DTYPE_BF16, n, R, "grads", f), _slabs(acc, CC_DTYPE_F32, n, R, "acc", f),
+        _vector(master, CC_DTYPE_F32, n, "master", f),
+        _vector(momentum, CC_DTYPE_F32, n, "momentum", f),
+        _slabs(params_out, CC_DTYPE_BF16, n, R, "params_out", f), n, R,
+        (_sz * max(1, count))(*offsets), count, rows, cols, lr, beta, int(bool(nesterov)),
+        weight_decay, update_scale, _coeffs(coeffs, steps), steps, eps, grad_scale,
+        _workspace(workspace, workspace_bytes, f), workspace_bytes, _stream(stream)), f)
 
 
 def cc_inject_launch_failure(after_launches: int) -> None:

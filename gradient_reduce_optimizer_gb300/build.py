@@ -3,13 +3,14 @@
 Each CUDA translation unit is compiled by nvcc in parallel into ``_build/``
 and linked into ``gradient_reduce_optimizer_gb300/libcc_dp.so`` with the
 CUDA runtime linked statically and cuBLAS (used only by the overlap
-measurement's proxy backward) dynamically.  The Python binding's C helper
-(``csrc/cc_calls.c``) becomes the extension module ``_calls.so``.  Host code is built with
+measurement's proxy backward) dynamically.  The Python binding's helper
+(``csrc/cc_calls.cpp``) becomes the extension module ``_calls.so``.  Host code is built with
 ``-ffp-contract=off`` so the AdamW scalars computed on the host are single
 binary32 roundings.  Run as a script, or call :func:`build`.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -64,28 +65,57 @@ def _stale(target: str, deps: List[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _calls_command(source: str, target: str) -> List[str]:
+    """The compiler's command for the extension module (torch's headers and
+    libraries are found without importing it)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise OSError("torch is not installed")
+    torch = os.path.dirname(spec.origin)
+    include = os.path.join(torch, "include")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared",
+            "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"], "-isystem", include,
+            "-isystem", os.path.join(include, "torch", "csrc", "api", "include"), "-I", INCLUDE,
+            source, "-o", target, "-L" + os.path.join(torch, "lib"), "-ltorch_python",
+            "-ltorch_cpu", "-lc10"]
+
+
+class _CallsBuild:
+    """The extension module's compilation, beside the others'."""
+
+    def __init__(self, force: bool):
+        source = os.path.join(CSRC, "cc_calls.cpp")
+        self.process, self.reason = None, ""
+        if force or _stale(CALLS, [source, os.path.join(INCLUDE, "cc_dp.h")]):
+            try:
+                self.process = subprocess.Popen(_calls_command(source, CALLS + ".tmp"),
+                                                stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
+                                                text=True)
+            except OSError as e:
+                self.reason = str(e)
+
+    def finish(self) -> str:
+        if self.process:
+            out, _ = self.process.communicate()
+            if self.process.returncode == 0:
+                os.replace(CALLS + ".tmp", CALLS)
+            else:
+                self.reason = f"{self.process.args[0]} gave {self.process.returncode}\n{out}"
+        if not self.reason:
+            return CALLS
+        if os.path.exists(CALLS):                 # one of older sources
+            os.remove(CALLS)
+        print(f"{os.path.basename(CALLS)} not built, layer norm calls take their arguments in "
+              f"Python: {self.reason.strip()}", file=sys.stderr)
+        return ""
+
+
 def build_calls(force: bool = False) -> str:
     """Compile (if stale) the binding's extension module; returns its path, or ""
-    where it cannot be built (it needs a C compiler and Python's headers): the
-    binding then takes its calls' arguments in Python, a few microseconds slower."""
-    source = os.path.join(CSRC, "cc_calls.c")
-    if force or _stale(CALLS, [source, os.path.join(INCLUDE, "cc_dp.h")]):
-        tmp = CALLS + ".tmp"
-        cmd = [os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-Wall", "-fPIC", "-shared",
-               "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, source, "-o", tmp]
-        try:
-            done = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-            reason = f"{cmd[0]} gave {done.returncode}\n{done.stdout}" if done.returncode else ""
-        except OSError as e:
-            reason = str(e)
-        if reason:
-            if os.path.exists(CALLS):             # one of older sources
-                os.remove(CALLS)
-            print(f"{os.path.basename(CALLS)} not built, layer norm calls take their arguments in "
-                  f"Python: {reason.strip()}", file=sys.stderr)
-            return ""
-        os.replace(tmp, CALLS)
-    return CALLS
+    where it cannot be built (it needs a C++ compiler and Python's and torch's
+    headers): the binding then takes its calls' arguments in Python, a few
+    microseconds slower."""
+    return _CallsBuild(force).finish()
 
 
 def build(force: bool = False, verbose: bool = False,
@@ -98,6 +128,7 @@ def build(force: bool = False, verbose: bool = False,
     """
     os.makedirs(build_dir, exist_ok=True)
     cc = nvcc()
+    calls = _CallsBuild(force) if library == LIBRARY else None
     objs, procs = [], []
     for src in SOURCES:
         path = os.path.join(CSRC, src)
@@ -128,8 +159,8 @@ def build(force: bool = False, verbose: bool = False,
         cmd += [f"-L{d}" for d in cuda_lib_dirs()]
         subprocess.run(cmd, check=True)
         os.replace(tmp, library)
-    if library == LIBRARY:
-        build_calls(force)
+    if calls:
+        calls.finish()
     return library
 
 

@@ -16,6 +16,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 from typing import Dict, List, Optional, Sequence, Tuple
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -538,15 +539,19 @@ def _calls():
         if not os.path.exists(path):
             _CALLS = _InPython
             return _CALLS
+        torch = _torch()              # whose libraries the module needs
         loader = importlib.machinery.ExtensionFileLoader("_calls", path)
-        module = importlib.util.module_from_spec(
-            importlib.util.spec_from_file_location("_calls", path, loader=loader))
-        loader.exec_module(module)
-        torch = _torch()
+        try:
+            module = importlib.util.module_from_spec(
+                importlib.util.spec_from_file_location("_calls", path, loader=loader))
+            loader.exec_module(module)
+        except ImportError as e:      # of another torch or Python
+            warnings.warn(f"{path}: {e}; layer norm calls take their arguments in Python")
+            _CALLS = _InPython
+            return _CALLS
         address = [ctypes.cast(fn, _vp).value
                    for fn in (lib().cc_layernorm_forward, lib().cc_layernorm_backward)]
-        module.setup(*address, (torch.bfloat16, torch.float16, torch.float32),
-                     torch.cuda.current_device, torch._C._cuda_getCurrentRawStream)
+        module.setup(*address, torch.cuda.current_device, torch._C._cuda_getCurrentRawStream)
         _CALLS = module
     return _CALLS
 

@@ -2,6 +2,7 @@
 way in, not a condition: without a compiler for it the build goes through, and
 without it the binding calls the library itself."""
 import os
+import warnings
 
 import pytest
 import torch
@@ -32,7 +33,9 @@ def test_the_build_goes_through_without_a_compiler_for_it(tmp_path, monkeypatch,
     assert calls.exists()
 
 
-def test_the_binding_works_without_it(monkeypatch):
+@pytest.mark.parametrize("there", [False, True])
+def test_the_binding_works_without_it(there, tmp_path, monkeypatch):
+    """Where it was not built, and where what is there cannot be loaded."""
     seen = []
 
     class Library:
@@ -40,13 +43,17 @@ def test_the_binding_works_without_it(monkeypatch):
         cc_layernorm_backward = staticmethod(lambda *a: seen.append(a) or 0)
 
     monkeypatch.setattr(capi, "_CALLS", None)
-    exists = os.path.exists
-    monkeypatch.setattr(os.path, "exists", lambda p: "_calls" not in str(p) and exists(p))
+    monkeypatch.setattr(capi, "__file__", str(tmp_path / "capi.py"))
+    if there:
+        (tmp_path / "_calls.so").write_bytes(b"no module")
     monkeypatch.setattr(capi, "lib", lambda: Library)
     monkeypatch.setattr(capi, "_stream", lambda s: 77)
     x, y = (torch.zeros(4, 16, dtype=torch.float16) for _ in range(2))
     w, m = torch.zeros(16), torch.zeros(4)
-    capi.cc_layernorm_forward(x, w, None, y, m, None, 4, 16, 1e-5)
+    with warnings.catch_warnings(record=True) as caught:
+        warnings.simplefilter("always")
+        capi.cc_layernorm_forward(x, w, None, y, m, None, 4, 16, 1e-5)
+    assert len(caught) == there
     capi.cc_layernorm_backward(y, x, w, m, m, y, None, None, 4, 16)
     assert seen[0][0] == x.data_ptr() and seen[0][-3:] == (capi.CC_DTYPE_F16, capi.CC_DTYPE_F32, 77)
     assert seen[1][0] == y.data_ptr() and seen[1][-1] == 77

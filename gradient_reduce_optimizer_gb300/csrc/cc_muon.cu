@@ -8,14 +8,19 @@
 // singular vectors; Muon's coefficients drive every one of them towards 1.
 //
 // Arithmetic.  The products run on the tensor cores on fp16 operands with
-// fp32 accumulation (cc_muon_gemm.cu).  Three things keep 11-bit operands
+// fp32 accumulation (cc_muon_gemm.cu).  What their roundings cost follows from the
+// singular values' spread (tests/test_gpu_muon_spectra.py has the formula, and
+// holds the kernels to 1.2 times it): 7e-4 of the result on a Gaussian matrix,
+// 6e-3 where one direction is all of it.  Three things keep 11-bit operands
 // accurate, each checked against 64 bits:
 //  * the first step reads G itself, not normalised: 16-bit matrices in place,
 //    fp32 ones (and the step's update) as bf16, which has their range, plus
 //    their rounding's own bf16 as a low part.  1/(|G|_F + eps) multiplies the
-//    accumulators.  bf16 operands cost nothing there: what the first products
+//    accumulators.  bf16 operands cost little there: what the first products
 //    add to a X is small next to it wherever singular values still have to
-//    grow (the result's error changes by less than 2%);
+//    grow (a Gaussian matrix's error changes by less than 2%; where one direction
+//    is all of the matrix, fp32's products of its bf16 part cost 5.7e-3, bf16's
+//    and fp16's own 3.6e-3 and 5.3e-3);
 //  * in all but the last two steps X carries a low part (the rounding of its
 //    fp16 value, itself in 8 bits, e5m2: three more bits of each element, and
 //    half the bytes of a second fp16) that joins the term a X.  There X's small

@@ -760,7 +760,7 @@ CC_API int cc_layernorm_backward_workspace(size_t rows, size_t cols, size_t *byt
  *   g              g_dtype; matrix i, row r, column c at
  *                  g[i * strideg + r * ldg + c].  Read.
  *   out            bf16, with strideo and ldo: written.  (bf16 is what the
- *                  iteration's accuracy fills: it is good to about 1e-3 of
+ *                  iteration's accuracy fills: it is good to 1e-3 to 6e-3 of
  *                  the result's norm, see below.)
  *   count, rows, cols   matrices and their shape; any 0: a no-op.  count at
  *                  most 65535, rows and cols at most 2^20.  The strides are
@@ -777,13 +777,20 @@ CC_API int cc_layernorm_backward_workspace(size_t rows, size_t cols, size_t *byt
  *
  * Arithmetic: the products take fp16 operands (scaled by powers of two, X with
  * a low part where that matters) and accumulate in fp32; the norm is the fp32
- * sum of squares.  The result of five steps is within about 1e-3 of its norm of
- * the exact one before it is rounded to bf16 (Muon's polynomial does not converge:
- * every further step multiplies what was rounded by up to 1.6).  A polynomial that lets singular values grow
- * far beyond 1 leaves fp16's range (X beyond 1000, A beyond 250) and gives
- * Inf or NaN; Muon's keeps them below 1.25.  A zero matrix gives zeros (with
- * eps > 0); NaN or Inf in a matrix gives NaN in all of it, and in it alone.  A
- * pipeline wait that runs out is reported by cc_device_status.
+ * sum of squares.  How far the result of Muon's five steps is from the exact one
+ * before it is rounded to bf16 (which adds 1.7e-3), relative to its norm, depends
+ * on how the singular values are spread: 7e-4 to 1e-3 for a Gaussian matrix or ones
+ * that fall as 1/k, 1.3e-3 for rank 8 plus 5 % noise, 1.8e-3 for 1/k^2, 3.5e-3
+ * for rank 8 plus 0.3 % noise, and at most 6e-3, where one direction holds all of
+ * the matrix.  (Roundings are relative to the large singular values, and small
+ * ones grow by up to 3.4 a step.)  Muon's polynomial does not converge: every step
+ * beyond the fifth multiplies that by up to 1.6.  Sides of at most 64 are computed
+ * in fp32.
+ * A polynomial that lets singular values grow far beyond 1 leaves fp16's range (X
+ * beyond 1000, A beyond 250) and gives Inf or NaN; Muon's keeps them below 1.25.  A
+ * zero matrix gives zeros (with eps > 0); NaN or Inf in a matrix gives NaN in all
+ * of it, and in it alone.  A pipeline wait that runs out is reported by
+ * cc_device_status.
  */
 #define CC_MUON_MAX_STEPS 16
 CC_API int cc_muon_orthogonalise(const void *g, size_t ldg, size_t strideg, void *out,

@@ -366,10 +366,17 @@ int make_plan(int count, int rows, int cols, Plan *p) {
     p->stride_a = p->lda * p->small;
     p->span = up(static_cast<size_t>(rows) * cols, 8);
     size_t at = 0;
+    bool fits = true;                    // (one matrix's parts are below 2^43 bytes)
     auto take = [&](size_t bytes_each) {
         const size_t here = at;
-        at += up(bytes_each * static_cast<size_t>(count), 256);
+        size_t all;
+        fits = fits && !__builtin_mul_overflow(bytes_each, static_cast<size_t>(count), &all) &&
+               all <= SIZE_MAX / 16;
+        at += fits ? up(all, 256) : 0;
         return here;
+    };
+    auto too_large = [&] {
+        return fail(CC_ERR_INVALID, "%d matrices of %d x %d are too large", count, rows, cols);
     };
     p->at_done = take(2 * sizeof(unsigned));
     p->at_partial = take(kMaxParts * sizeof(float));
@@ -380,7 +387,7 @@ int make_plan(int count, int rows, int cols, Plan *p) {
         p->at_gram = take(square * small_parts(count, std::max(rows, cols)));
         p->at_q = take(square);
         p->bytes = at;
-        return CC_OK;
+        return fits ? CC_OK : too_large();
     }
     p->at_x0 = take(2 * p->stride);
     p->at_x1 = take(2 * p->stride);
@@ -394,7 +401,7 @@ int make_plan(int count, int rows, int cols, Plan *p) {
     p->at_split = at;
     if (p->has_split) at += kMostPieces * kPieceBytes;
     p->bytes = at;
-    return CC_OK;
+    return fits ? CC_OK : too_large();
 }
 
 // CTAs a matrix for the elementwise passes: two vectors of 8 elements a

@@ -66,3 +66,15 @@ def test_step():
         refused(step, f"{name} is", **{name: lambda t: t.to(BF16)})
         refused(step, f"{name} must", **{name: lambda t: t[1:]})
     refused(step, "workspace", workspace=lambda t: t[1:])
+
+
+def test_workspace_that_does_not_fit_in_64_bits():
+    """2^31 - 1 of the largest matrices are refused; the most that a call takes
+    are not."""
+    side = 1 << 20
+    assert capi.cc_muon_workspace(65535, side, side) > 65535 * 11 * side * side
+    for count, rows, cols in (((1 << 31) - 1, side, side), (1 << 22, side, side),
+                              ((1 << 31) - 1, side, side // 2)):
+        with pytest.raises(capi.CCError) as e:
+            capi.cc_muon_workspace(count, rows, cols)
+        assert e.value.status == capi.CC_ERR_INVALID and "too large" in e.value.reason

@@ -150,6 +150,7 @@ _SIGNATURES = {
                           _vp, _i, _f, _f, _vp, _sz, _vp], _i),
     "cc_inject_bulk_stall": ([ctypes.c_longlong, ctypes.c_uint], _i),
     "cc_inject_layernorm_stall": ([ctypes.c_longlong, ctypes.c_uint], _i),
+    "cc_inject_muon_stall": ([_i, ctypes.c_uint], _i),
     "cc_inject_launch_failure": ([_i], _i),
     "cc_tp_overlap_bench": ([ctypes.POINTER(cc_tp_cfg), ctypes.POINTER(cc_tp_result)], _i),
 }
@@ -806,6 +807,13 @@ def cc_inject_layernorm_stall(row: int, timeout_us: int = 20000) -> None:
     """Skip the copies of row `row` (-1 disarms) in this thread's next layer
     norm backward launch, with its waits bounded by timeout_us."""
     _check(lib().cc_inject_layernorm_stall(row, timeout_us), "cc_inject_layernorm_stall")
+
+
+def cc_inject_muon_stall(matrix: int, timeout_us: int = 20000) -> None:
+    """Keep matrix `matrix` (-1 disarms) from its second product in this
+    thread's next orthogonalisation on the tensor cores, with its waits for
+    other tiles bounded by timeout_us."""
+    _check(lib().cc_inject_muon_stall(matrix, timeout_us), "cc_inject_muon_stall")
 
 
 def cc_l2_flush(buf, nbytes: int, stream=None) -> None:

@@ -710,6 +710,14 @@ int cc_inject_layernorm_stall(long long row, unsigned timeout_us) {
     return CC_OK;
 }
 
+int cc_inject_muon_stall(int matrix, unsigned timeout_us) {
+    if (matrix < -1) return fail(CC_ERR_INVALID, "matrix=%d must be >= -1", matrix);
+    if (matrix >= 0 && (timeout_us < 1 || timeout_us > 1000000))
+        return fail(CC_ERR_INVALID, "timeout_us=%u must be in 1..1000000", timeout_us);
+    arm_muon_stall(matrix, 1000ull * timeout_us);
+    return CC_OK;
+}
+
 int cc_device_status(unsigned *status, int clear) {
     if (!status) return fail(CC_ERR_INVALID, "status is NULL");
     int st = ensure_device();

@@ -125,6 +125,10 @@ cudaError_t read_ln_status(unsigned *status, bool clear);
 // never issued, and the launch's waits give up after limit_ns.  row < 0 disarms.
 void arm_layernorm_stall(long long row, unsigned long long limit_ns);
 
+// The same of this thread's next launch of the orthogonalisation's products: matrix
+// `matrix` of the batch never gets to its second product.  matrix < 0 disarms.
+void arm_muon_stall(int matrix, unsigned long long limit_ns);
+
 // Multiprocessor count of the current device (queried once per device).
 cudaError_t device_sm_count(int *count);
 

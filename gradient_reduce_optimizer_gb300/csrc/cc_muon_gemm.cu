@@ -146,6 +146,8 @@ struct Params {
     float *split;
     unsigned *split_done;                // of each matrix
     unsigned split_counts;               // what a product's pieces add to it
+    int stall;                           // a matrix whose counter never gets there, or -1
+    unsigned long long limit_ns;         // of a wait for a counter
 };
 
 // ---- building blocks ----------------------------------------------------------
@@ -357,6 +359,7 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Place &a) {
         t.m0 = divide(r, p.tiles_xn, p.inv_tiles_xn, j) * 256;
         t.n0 = j * t.bn;
     }
+    if (t.b == p.stall && t.ready > 0) t.ready = 0xFFFFFFFFu;      // failure injection
     return t;
 }
 
@@ -439,27 +442,26 @@ __device__ __forceinline__ uint32_t instruction(const Params &p, const Tile &t,
 }
 
 // A matrix's counter, and the wait until it reaches `target` (at most about
-// kTimeoutNs).
+// limit_ns).
 __device__ __forceinline__ unsigned progress(const unsigned *done) {
     unsigned v;
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(done) : "memory");
     return v;
 }
-__device__ __forceinline__ bool wait_progress(const unsigned *done, unsigned target) {
+__device__ __forceinline__ bool wait_progress(const unsigned *done, unsigned target,
+                                              unsigned long long limit_ns) {
     if (progress(done) >= target) return true;
     const unsigned long long t0 = global_ns();
     while (progress(done) < target) {
-        if (global_ns() - t0 > kTimeoutNs) return false;
+        if (global_ns() - t0 > limit_ns) return false;
         __nanosleep(32);
     }
     return true;
 }
 
 // A wait that can last as long as several others in turn.
-__device__ __forceinline__ bool long_wait(uint32_t bar, uint32_t parity) {
-    for (int i = 0; i < 4; ++i)
-        if (mbar_wait(bar, parity)) return true;
-    return false;
+__device__ __forceinline__ bool long_wait(const Params &p, uint32_t bar, uint32_t parity) {
+    return mbar_wait(bar, parity, 4 * p.limit_ns);
 }
 
 // ---- operands -------------------------------------------------------------------
@@ -667,7 +669,8 @@ __device__ __forceinline__ bool pieces_there(const Params &p, const Tile &t, int
         there = wait_progress(
             p.split_done + t.b,
             static_cast<unsigned>(p.cut_p.pieces > 1 ? 2 * t.k + t.kind + 1 : t.k + 1) *
-                p.split_counts);
+                p.split_counts,
+            p.limit_ns);
     there = __all_sync(0xFFFFFFFFu, there) != 0;
     __syncwarp();                        // orders the other lanes' reads behind lane 0's acquire
     return there;
@@ -923,13 +926,13 @@ ns_kernel(const __grid_constant__ Params p, const __grid_constant__ FINAL final_
             // Put tile n_tile into the ring for the other warps.
             auto publish = [&]() {
                 const uint32_t slot = n_tile % kAhead, lap = n_tile / kAhead;
-                if (lap > 0 && !long_wait(smem_u32(&input_seen[slot]), (lap - 1) & 1)) return false;
+                if (lap > 0 && !long_wait(p, smem_u32(&input_seen[slot]), (lap - 1) & 1)) return false;
                 ring[slot] = Job{t, o.kb, instruction(p, t, o), o.a_mn, o.b_mn, o.once};
                 return true;
             };
             if (first < p.jobs) ok = publish();
             for (int job = first; ok && job < p.jobs; job += stride) {
-                if (!known && !wait_progress(p.done + t.b, t.ready)) {
+                if (!known && !wait_progress(p.done + t.b, t.ready, p.limit_ns)) {
                     ok = false;
                     break;
                 }
@@ -982,7 +985,7 @@ ns_kernel(const __grid_constant__ Params p, const __grid_constant__ FINAL final_
             for (int job = first; ok && job < p.jobs; job += stride, ++n_tile) {
                 const uint32_t acc = n_tile & 1u, acc_use = n_tile >> 1;
                 const uint32_t slot = n_tile % kAhead;
-                if (!long_wait(smem_u32(&input_ready[slot]), (n_tile / kAhead) & 1)) {
+                if (!long_wait(p, smem_u32(&input_ready[slot]), (n_tile / kAhead) & 1)) {
                     atomicOr(&g_muon_status, kStatusMma);
                     break;
                 }
@@ -1040,7 +1043,7 @@ ns_kernel(const __grid_constant__ Params p, const __grid_constant__ FINAL final_
                 // No tile is counted before all it depends on is: a counter never
                 // runs ahead.
                 const uint32_t slot = n_tile % kAhead;
-                ok = long_wait(smem_u32(&input_ready[slot]), (n_tile / kAhead) & 1);
+                ok = long_wait(p, smem_u32(&input_ready[slot]), (n_tile / kAhead) & 1);
                 const Tile t = ring[slot].t;
                 if (ok) mbar_arrive(smem_u32(&input_seen[slot]));
                 // the last step's results leave otherwise, and nobody waits for them;
@@ -1059,7 +1062,7 @@ ns_kernel(const __grid_constant__ Params p, const __grid_constant__ FINAL final_
                     int q = 0;
                     for (; ok && q < 4 && row0 + 32 * q < m; ++q) {
                         const int e = 4 * h + q;
-                        ok = long_wait(smem_u32(&out_full[e]), (parity >> q) & 1);
+                        ok = long_wait(p, smem_u32(&out_full[e]), (parity >> q) & 1);
                         if (!ok) break;
                         parity ^= 1u << q;
                         const uint32_t mine = boxes + static_cast<uint32_t>(e * kWarpBytes);
@@ -1104,7 +1107,7 @@ ns_kernel(const __grid_constant__ Params p, const __grid_constant__ FINAL final_
         for (int job = first; ok && job < p.jobs; job += stride, ++n_tile) {
             const uint32_t slot = n_tile % kAhead;
             ok = __all_sync(0xFFFFFFFFu,
-                            long_wait(smem_u32(&input_ready[slot]), (n_tile / kAhead) & 1));
+                            long_wait(p, smem_u32(&input_ready[slot]), (n_tile / kAhead) & 1));
             if (!ok) break;
             const Tile t = ring[slot].t;
             __syncwarp();
@@ -1137,7 +1140,7 @@ ns_kernel(const __grid_constant__ Params p, const __grid_constant__ FINAL final_
             if (ok) {
                 load(e / 4);
                 ok = __all_sync(0xFFFFFFFFu,
-                                long_wait(smem_u32(&acc_full[acc]), (n_tile >> 1) & 1));
+                                long_wait(p, smem_u32(&acc_full[acc]), (n_tile >> 1) & 1));
             }
             if (!ok) break;
             tc_fence_after();
@@ -1291,7 +1294,8 @@ ns_kernel(const __grid_constant__ Params p, const __grid_constant__ FINAL final_
         if (!ok && lane == 0) {
             atomicOr(&g_muon_status, kStatusEpilogue);
             // a wait ran out: give the copies in flight time to land
-            if (!mbar_wait(smem_u32(&in_full[e]), in_parity)) atomicOr(&g_muon_status, kStatusDrain);
+            if (!mbar_wait(smem_u32(&in_full[e]), in_parity, p.limit_ns))
+                atomicOr(&g_muon_status, kStatusDrain);
         }
         __syncwarp();
     }
@@ -1431,6 +1435,11 @@ void choose_widths(Params &p, int clusters) {
     }
 }
 
+// One-shot injected stall of this thread's next launch (cc_inject_muon_stall): the
+// matrix whose second product never starts, or -1, and the limit of the waits.
+thread_local int g_stall_matrix = -1;
+thread_local unsigned long long g_stall_ns = 0;
+
 template <typename FINAL>
 int iterate(const Iteration &it, const FINAL &out, cudaStream_t stream) {
     int sms = 0;
@@ -1449,6 +1458,9 @@ int iterate(const Iteration &it, const FINAL &out, cudaStream_t stream) {
     p.parts = it.parts;
     p.eps = it.eps;
     p.done = it.done;
+    p.stall = g_stall_matrix;
+    p.limit_ns = g_stall_matrix >= 0 ? g_stall_ns : kTimeoutNs;
+    g_stall_matrix = -1;
     for (int k = 0; k < it.steps; ++k) {
         const float *c = it.coeffs + 3 * k;
         // near the end, but not before the singular values have grown (k = 2)
@@ -1552,6 +1564,11 @@ int iterate_step(const Iteration &it, const StepOut &out, cudaStream_t stream) {
 }
 
 }  // namespace muon
+
+void arm_muon_stall(int matrix, unsigned long long limit_ns) {
+    muon::g_stall_matrix = matrix;
+    muon::g_stall_ns = limit_ns;
+}
 
 cudaError_t read_muon_status(unsigned *status, bool clear) {
     cudaError_t e = cudaMemcpyFromSymbol(status, g_muon_status, sizeof(unsigned));

@@ -850,9 +850,10 @@ CC_API int cc_muon_workspace(int count, int rows, int cols, size_t *bytes);
  * and returns instead of hanging).  Bulk-copy engine (one second per wait):
  * 1 consumer, 2 producer, 4 drain of copies in flight.  Fused tensor-parallel
  * kernel (two seconds): 8 producer, 16 MMA, 32 epilogue, 64 drain.  The
- * orthogonalisation's products (two seconds): 256 producer, 512 MMA, 1024
- * epilogue, 2048 drain.  Layer norm (two seconds): 4096, a row's copies (dx of
- * rows not reached, dweight and dbias are then left as they were).  Builds
+ * orthogonalisation's products (two seconds; eight for waits that last as long
+ * as others in turn): 256 producer, 512 MMA, 1024 epilogue, 2048 drain.  Layer
+ * norm (two seconds): 4096, a row's copies (dx of rows not reached, dweight and
+ * dbias are then left as they were).  Builds
  * with CC_DEBUG_BOUNDS=1 only: 128, an access of either kernel fell outside
  * the buffer or range its arguments describe and was skipped.  A non-zero
  * word means some launch did not finish its range.  Synchronises with the
@@ -901,6 +902,20 @@ CC_API int cc_inject_bulk_stall(long long tile, unsigned timeout_us);
  * code 4096.  row = -1 disarms.
  */
 CC_API int cc_inject_layernorm_stall(long long row, unsigned timeout_us);
+
+/*
+ * cc_inject_muon_stall -- the same for the orthogonalisation's products.  Arms a
+ * one-shot for the calling thread: in its next cc_muon_orthogonalise or
+ * cc_fused_dp_muon call on matrices of more than 64 a side, matrix `matrix` of the
+ * batch never gets to its second product, and the waits for products give up after
+ * timeout_us (1..1000000; four times that, for those that wait for such a wait).
+ * Clusters of CTAs leave when they come to that matrix, others when they come to
+ * what those did not do.  This matrix's results (out; or the master weights and
+ * parameters) keep their contents, other matrices' are written in part or whole,
+ * and cc_device_status reports codes of 256 to 2048.
+ * matrix = -1 disarms.
+ */
+CC_API int cc_inject_muon_stall(int matrix, unsigned timeout_us);
 
 /*
  * cc_l2_flush -- overwrite `bytes` of the caller's device buffer `buf`

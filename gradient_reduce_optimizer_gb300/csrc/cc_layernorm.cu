@@ -8,9 +8,9 @@
 //   y    = (s - mean) * rstd * weight + bias
 // The row stays in registers between the two sums, so the variance is the
 // exact two-pass form (no cancellation of E[s^2] - mean^2) at one read.  The
-// second pass also sums s - mean, which is what the first one's roundings left:
-// it corrects the mean, the variance and y.  (In a row that is all but constant
-// rstd is up to 1/sqrt(eps), and would make much of an ulp of the mean.)
+// second pass also sums s - mean, which is what the first one's roundings left: in
+// a row that is all but constant it corrects the mean, the variance and y.  (rstd
+// is up to 1/sqrt(eps) there, and would make much of an ulp of the mean.)
 //
 // Backward, with h = (x - mean) * rstd and t = dy * weight:
 //   dx = rstd * (t - mean(t) - h * mean(t * h)) (+ dsum)
@@ -263,14 +263,19 @@ __device__ __forceinline__ float2 group_sum2(float a, float b, float2 *buf, int 
 
 // A row's statistics from its first mean m and the sums of the deviations d from
 // it and of their squares: the mean, 1 / sqrt(variance + eps), and the shift that
-// makes d * rstd + shift the normalised element.
+// makes d * rstd + shift the normalised element.  m is off by some ulps of the
+// row's largest elements, the mean c of the deviations by some of theirs: c
+// corrects m where they are small next to it (a deviation below |m| / 16), and
+// would only add its own roundings to it elsewhere.
 struct RowStats {
     float mean, rstd, shift;
 };
 __device__ __forceinline__ RowStats row_stats(float m, float sum_d, float sum_d2, float inv_cols,
                                               float eps) {
-    const float c = sum_d * inv_cols;
-    float var = __fmaf_rn(-c, c, sum_d2 * inv_cols);
+    float c = sum_d * inv_cols;
+    float var = sum_d2 * inv_cols;
+    if (!(256.0f * var < m * m)) c = 0.0f;
+    var = __fmaf_rn(-c, c, var);
     if (var < 0.0f) var = 0.0f;                       // a rounding; NaN stays
     const float rstd = __frsqrt_rn(var + eps);
     return {m + c, rstd, -c * rstd};

@@ -103,3 +103,22 @@ def test_one_element_apart():
         x[1, 0] -= 2.0 ** -21
         x[2, cols // 2] += 1e-3
         check(x, torch.ones(cols, device=DEV), torch.zeros(cols, device=DEV))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=str)
+@pytest.mark.parametrize("cols", COLS)
+def test_the_mean_of_a_row_whose_sum_is_exact(cols, dtype):
+    """Integers: every partial sum is one below 2^24, so the mean is off by the
+    quotient's roundings alone (1 / cols' and the product's), however small it is
+    next to the elements, and in rows that vary little too."""
+    g = torch.Generator(device=DEV).manual_seed(cols + 2)
+    x = torch.randint(-100, 101, (40, cols), generator=g, device=DEV).float()
+    x[20:] = 100 + torch.randint(-1, 2, (20, cols), generator=g, device=DEV)
+    x = x.to(dtype)
+    mean = torch.empty(40, device=DEV)
+    capi.cc_layernorm_forward(x, None, None, torch.empty_like(x), mean, None, 40, cols, 1e-5)
+    want = x.double().mean(1)
+    error = (mean.double() - want).abs()
+    assert (error[:20] <= 2.01 * U * want[:20].abs()).all()
+    # corrected by the deviations' mean, itself within (80 + cols / 256) u of them
+    assert (error[20:] <= U * want[20:].abs() + 2 * (80 + cols / 256) * U).all()

@@ -187,9 +187,24 @@ small_iterate_kernel(const float *partial, int parts, int m, float eps,
                 put(T, u);
             }
             __syncthreads();
+            // P (A P), of which one triangle counts for both: outer() reads its first
+            // operand across, and an A that its roundings have made unsymmetric goes
+            // astray from step to step (a matrix of rank one came out 8e-3 off, and so
+            // 2e-4).
             float w[4][4] = {};
-            if (mine) {
-                outer(P, T, m, i, j, w);              // P (A P)
+            if (mine && j >= i) {
+                outer(P, T, m, i, j, w);
+                if (i == j) {
+#pragma unroll
+                    for (int r = 1; r < 4; ++r)
+#pragma unroll
+                        for (int s = 0; s < r; ++s) w[r][s] = w[s][r];
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        *reinterpret_cast<float4 *>(&A[4 * j + s][4 * i]) =
+                            make_float4(w[0][s], w[1][s], w[2][s], w[3][s]);
+                }
                 put(A, w);
             }
         }
@@ -198,7 +213,7 @@ small_iterate_kernel(const float *partial, int parts, int m, float eps,
     float *out = q_out + static_cast<size_t>(blockIdx.x) * kM * kM;
     for (int e = threadIdx.x; e < kM * kM; e += kThreads) {
         const int r = e / kM, s = e % kM;
-        out[e] = r < m && s < m ? Q[r][s] * inv : 0.0f;
+        out[e] = r < m && s < m ? Q[s][r] * inv : 0.0f;   // as outer() reads it
     }
 }
 
@@ -222,7 +237,7 @@ small_apply_kernel(const __grid_constant__ SmallSource s, const float *q_in,
         for (int e = threadIdx.x; e < kM * kM; e += kThreads) xt[e % kM][e / kM] = tile[e / kM][e % kM];
         __syncthreads();
         float c[4][4] = {};
-        outer(q, xt, s.m, i, j, c);                    // Q is symmetric
+        outer(q, xt, s.m, i, j, c);                    // q: Q across
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < 4; ++r)

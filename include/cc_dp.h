@@ -785,7 +785,7 @@ CC_API int cc_layernorm_backward_workspace(size_t rows, size_t cols, size_t *byt
  * the matrix.  (Roundings are relative to the large singular values, and small
  * ones grow by up to 3.4 a step.)  Muon's polynomial does not converge: every step
  * beyond the fifth multiplies that by up to 1.6.  Sides of at most 64 are computed
- * in fp32.
+ * in fp32: 1e-6 for a Gaussian matrix, at most 1e-3 for the others.
  * A polynomial that lets singular values grow far beyond 1 leaves fp16's range (X
  * beyond 1000, A beyond 250) and gives Inf or NaN; Muon's keeps them below 1.25.  A
  * zero matrix gives zeros (with eps > 0); NaN or Inf in a matrix gives NaN in all

@@ -166,3 +166,57 @@ def test_step(m, n, kind):
     want = exact(update)
     error = ((-master.double().view(m, n) - want).norm() / want.norm()).item()
     assert error <= 1.2 * expected_error(update, 8)
+
+
+# ---- a side of at most 64: fp32 --------------------------------------------------
+
+
+def expected_error_small(g):
+    """There every iterate is Q(A) G, Q the steps' polynomial of the first Gram
+    matrix A alone, with eigenvalues l = s^2.  A's entries are off by rms 2^-24 0.43
+    a rounding over chains of some 64, evenly over the eigenvectors' basis: element
+    (i, j) reaches the result as the divided difference of Q at l_i and l_j times
+    s_j.  Q's own entries are off by as much of Q, which is a^5 = 485 on the small
+    singular values."""
+    s = torch.linalg.svdvals(g.double())
+    s = s / s.norm()
+    eig, m = s * s, len(s)
+
+    def polynomial(l):
+        q, x = torch.ones_like(l), l
+        for _ in range(STEPS):
+            f = a + b * x + c * x * x
+            q, x = q * f, x * f * f
+        return q
+
+    i, j = eig[:, None], eig[None, :]
+    q = polynomial(eig)
+    at = eig.clone().requires_grad_(True)
+    slope = torch.autograd.grad(polynomial(at).sum(), at)[0]
+    divided = torch.where((i - j).abs() <= 1e-7 * (i + j), ((slope[:, None] + slope) / 2),
+                          (q[:, None] - q[None, :]) / (i - j))
+    unit = 2.0 ** -24 * 0.43 * 8
+    through_a = unit * eig.norm() / m * (divided * s[None, :]).norm()
+    through_q = unit * q.norm() / math.sqrt(m)
+    return (torch.hypot(through_a, through_q) / (q * s).norm()).item()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("m,n", [(64, 200), (200, 60), (33, 70), (16, 400)])
+def test_step_of_few_rows(m, n, kind):
+    """In fp32, by the step.  Four times the estimate, which takes the chains'
+    lengths from their order of size alone, and 1e-5 for the roundings that it leaves
+    out (of G's product with Q, a few 2^-24 of the result each)."""
+    g = torch.Generator(device=DEV).manual_seed(m + n + 2)
+    momentum = matrix(kind, m, n, g).flatten().contiguous()
+    update = (momentum * 0.25).view(m, n)
+    master = torch.zeros(m * n, device=DEV)
+    grads = [torch.zeros(m * n, device=DEV, dtype=torch.bfloat16)]
+    out = [torch.empty(m * n, device=DEV, dtype=torch.bfloat16)]
+    nb = capi.cc_muon_workspace(1, m, n)
+    ws = torch.empty(nb, device=DEV, dtype=torch.uint8)
+    capi.cc_fused_dp_muon(grads, None, master, momentum, out, m * n, 1, [0], m, n, ws, nb, lr=1.0,
+                          beta=0.5, eps=0.0)
+    want = exact(update)
+    error = ((-master.double().view(m, n) - want).norm() / want.norm()).item()
+    assert error <= 4 * expected_error_small(update) + 1e-5

@@ -295,9 +295,9 @@ struct FwdArgs {
 // which keeps 64 bytes (128 with a residual) a thread on their way and leaves room
 // for 24 and more warps an SM.  Rows are not walked by persistent CTAs here: with
 // little state to a row, new CTAs hide more latency than a ring of stages did
-// (16384 x 1024: 32 us).  16384 x 1024 bf16 with residual and sum in 24.6 us, 5.5
-// TB/s; 8192 x 3072 fp32 in 33.7 us, 6.0 TB/s (a device copy of as many bytes takes
-// 1.5 us less); 512 x 1024 in 4.9 us, which is the call's time on the CPU.
+// (16384 x 1024: 32 us).  16384 x 1024 bf16 with residual and sum in 24.5 us, 5.5
+// TB/s; 8192 x 3072 fp32 in 34.2 us, 5.9 TB/s (a device copy of as many bytes takes
+// 2 us less); 512 x 1024 in 3.9 us, which is the call's time on the CPU.
 template <typename T, int NV, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kFwdWarps)
 ln_fwd_kernel(const __grid_constant__ FwdArgs<T> p) {
@@ -401,11 +401,9 @@ ln_fwd_kernel(const __grid_constant__ FwdArgs<T> p) {
 // are 32 elements side by side wherever the row starts; they cost more
 // instructions than vectors, but no masks, no shifts and no edges.  (The
 // aligned vectors that a row touches, masked at its ends, were slower: 16384 x
-// 1023 bf16 with its residual took 66 us, this takes 39; of 1024, 24.)
-constexpr int kScalarMost = 640;        // of eight elements a thread: two CTAs an SM
+// 1023 bf16 with its residual took 66 us, this takes 40; of 1024, 24.)
 template <typename T, int NE, bool BLOCK>
-__global__ void __launch_bounds__(!BLOCK ? 32 * kFwdWarps : NE == 8 ? kScalarMost : 1024,
-                                  BLOCK && NE == 8 ? 2 : 1)
+__global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kFwdWarps)
 ln_fwd_scalar_kernel(const __grid_constant__ FwdArgs<T> p) {
     __shared__ float buf[BLOCK ? 128 : 1];
     const int L = BLOCK ? static_cast<int>(blockDim.x) : 32;
@@ -472,7 +470,7 @@ ln_fwd_scalar_kernel(const __grid_constant__ FwdArgs<T> p) {
     // Loads of parameters do not overtake stores of y; where a thread has many, all
     // of them come first (bf16, us, first and in turn: 16384 x 333 11.1 and 13.2,
     // 3001 x 8191 65 and 74; with eight a warp's lane 20000 x 61 6.8 and 6.3).
-    constexpr bool kAllFirst = BLOCK || NE > 8;
+    constexpr bool kAllFirst = NE > 8;
     // the parameters' types, told apart once
     auto finish = [&](auto weight, auto bias) {
 #pragma unroll
@@ -653,8 +651,8 @@ constexpr int bwd_threads(int elements, bool hold) {
 }
 constexpr int kMostGroups = 15;         // named barriers 1 to 15
 
-// 16384 x 1024 bf16 with dsum in 28.9 us with the columns' kernel, 4.6 TB/s; 8192 x
-// 3072 fp32 in 57.5 us, 5.2 TB/s; 512 x 1024 in 7.9 us.  What is left of the large
+// 16384 x 1024 bf16 with dsum in 30.1 us with the columns' kernel, 4.5 TB/s; 8192 x
+// 3072 fp32 in 55.4 us, 5.5 TB/s; 512 x 1024 in 8.1 us.  What is left of the large
 // ones is the tail: the columns' sums across warps, then the second launch (4 to 5
 // us of the GPU's time, half of it hidden).
 //
@@ -974,7 +972,9 @@ ln_bwd_kernel(const __grid_constant__ BwdArgs<T> p, int warps, int stages) {
 
 // Any shape, alignment and row stride: one CTA a row at a time, element by
 // element; the column sums live in the CTA's own row of the workspace, where
-// each column is always the same thread's.
+// each column is always the same thread's.  Their traffic, and one element an
+// access, make it slow: 16384 x 1024 bf16 with dsum, rows 1027 elements apart, 275
+// us; 2000 x 16392 725 (of 16384 in vectors 86).
 template <typename T>
 __global__ void __launch_bounds__(kScalarThreads)
 ln_bwd_any_kernel(const __grid_constant__ BwdArgs<T> p) {
@@ -1082,11 +1082,10 @@ Shape forward_shape(size_t rows, size_t cols, size_t elem, Rows how) {
     s.kind = vector ? Shape::kVector : Shape::kScalar;
     const size_t n = vector ? cols * elem / 16 : cols;
     if (vector) s.nv = n <= 32 ? 1 : n <= 64 ? 2 : 4;
-    // Element by element: more threads a row hide more latency, until the sums over
-    // a CTA cost more (bf16, us, 8 and 16 elements a thread: 16384 x 333 17.5
-    // (two warps) and 12.0 (one); 2000 x 5001 29.7 and 31.6; 3001 x 8191 84 and
-    // 71; 32 elements on one warp: 16384 x 1023 51, 8 on four 40).
-    else s.nv = n <= 256 ? 8 : n <= 512 ? 16 : n <= 8 * kScalarMost ? 8 : 16;
+    // Element by element: sixteen a thread, and eight where a warp does (bf16, us,
+    // sixteen and eight: 16384 x 333 10.4 and, in two warps, 17.4; 16384 x 1023 39.7
+    // and 39.0; 2000 x 5001 27.5 and 29.2).
+    else s.nv = n <= 256 ? 8 : 16;
     s.threads = threads_of(n, s.nv);
     s.warps = s.threads / 32;
     // few rows: over all SMs, rather than all a CTA's warps
@@ -1197,8 +1196,7 @@ cudaError_t launch_fwd(const FwdArgs<T> &a, Rows how, cudaStream_t stream) {
     if (s.kind == Shape::kAny)
         return launch(ln_fwd_any_kernel<T>, dim3(s.grid), s.threads, 0, stream, a);
     if (s.kind == Shape::kScalar) {
-        auto kernel = s.warps > 1 ? (s.nv == 8 ? ln_fwd_scalar_kernel<T, 8, true>
-                                                 : ln_fwd_scalar_kernel<T, 16, true>)
+        auto kernel = s.warps > 1  ? ln_fwd_scalar_kernel<T, 16, true>
                       : s.nv == 8 ? ln_fwd_scalar_kernel<T, 8, false>
                                   : ln_fwd_scalar_kernel<T, 16, false>;
         return launch(kernel, dim3(s.grid), s.threads, 0, stream, a);

@@ -40,18 +40,19 @@
 //   * results leave by TMA, issued by two more warps for four epilogue warps
 //     each, which also wait until they are in memory and then count the tile.
 // What bounds it.  A k-block costs about 2.7 cycles for each 128-byte row of
-// operands that the SM's copy engine takes in (256 rows of a 256 x 256 tile: 690
-// cycles, where the tensor cores take 512), which is cuBLAS's own rate: a step of
-// 96 x 1024^2 takes 345 us, three cuBLAS batches of its full products 490.  One
-// product of a single 1024^2 matrix takes 9 us: 3.6 for the k-blocks, the rest from
-// the last one through epilogue, store, counter and the first loads of the next.
-// A tile's epilogue has to stay below its products (16 k-blocks for K = 1024).  What it costs is latency, not
-// instructions: a copy instruction queues behind the operands' (about 450
-// cycles), so it moves 4 KiB; and waiting for stores in flight (1500 to 4000
-// cycles) is not the epilogue warps' business.
+// operands that the SM's copy engine takes in: 256 rows of a 256 x 256 tile 690
+// cycles, where the tensor cores take 512 (and cuBLAS's 8192^3 product, at 1,706
+// TFLOP/s and 1,455 MHz, about 545).  One product of a single 1024^2 matrix takes
+// 9 us: 3.6 for the k-blocks, the rest from the last one through epilogue, store,
+// counter and the first loads of the next.
+// A tile's epilogue has to stay below its products (16 k-blocks for K = 1024).
+// What it costs is latency, not instructions: a copy instruction queues behind the
+// operands' (about 450 cycles), so it moves 4 KiB; and waiting for stores in flight
+// (1500 to 4000 cycles) is not the epilogue warps' business.
 //
-// Ragged sizes need no padding: TMA fills what lies outside a matrix with
-// zeros and clips what is stored there.
+// Ragged sizes: TMA fills what lies outside a matrix with zeros and clips what is
+// stored there.  It does so at whole 16 bytes, so the workspace's matrices have
+// their rows filled up with zeros to there, and maps that end there.
 
 #include <cuda.h>
 #include <cuda_fp16.h>

@@ -3,7 +3,7 @@
 //
 // Two things differ from the tensor-core path.  A tile of the tensor cores is
 // 128 wide, so such matrices would leave most of it empty over fifteen
-// dependent launches; and the roundings of 11-bit operands average out over m
+// dependent products; and the roundings of 11-bit operands average out over m
 // rows, which few rows do not do (up to 1e-2 of the result at m = 3).  Here
 // every iterate is a polynomial of the first Gram matrix, X_k = Q_k X_0 with
 // Q_k and A_k = X_k X_k^T both m x m and commuting:
@@ -15,8 +15,11 @@
 //   apply    Q G, to bf16 or into the parameters.
 // In fp32 the Gram matrix resolves singular values down to 2^-12 of the
 // largest, the same relative to which their growth by a^steps stays small; the
-// 11-bit path could not do this (it would need its A to 2^-22).
+// 11-bit path could not do this (it would need its A to 2^-22).  1e-6 of the result
+// off on Gaussian matrices, up to 7e-4 where singular values lie there.
 //
+// What bounds it is the iterate kernel's chain of products: 7 x 64 x 2744 fp32 takes
+// 75 us, 60 x 64 x 300 68, a step of 7 x 64 x 2744 with eight replicas 99.
 // m = 64 takes 17 products of 64^3 in one CTA, 64 x (two 16-byte reads, 16
 // FMAs) a thread each.
 

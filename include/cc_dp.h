@@ -686,7 +686,8 @@ CC_API int cc_tp_matmul_allreduce_workspace(int m, int n, int k, int R, int max_
  *   mean = sum(s) / cols
  *   rstd = 1 / sqrt(sum((s - mean)^2) / cols + eps)
  *   y    = (s - mean) * rstd * weight + bias
- * computed in fp32 (two passes over the row on chip) and rounded once.
+ * computed in fp32 (two passes over the row on chip, the second correcting the
+ * mean of a row that varies little) and rounded once.
  * NaN and Inf propagate within their row.
  *
  *   x, y           act_dtype, rows x cols; row i at x + i * ldx elements
@@ -701,9 +702,10 @@ CC_API int cc_tp_matmul_allreduce_workspace(int m, int n, int k, int R, int max_
  *   act_dtype, param_dtype   CC_DTYPE_*, independent of each other.
  * Pointers need the alignment of their element only (CC_ERR_MISALIGNED); rows of
  * at most 16384 elements whose bases, strides and lengths are multiples of 16
- * bytes are fastest, others of at most 16384 take up to twice their time.
- * Written ranges overlap nothing else (CC_ERR_ALIAS).  One launch; allocates
- * nothing.
+ * bytes are fastest, others of at most 16384 take up to twice their time, longer
+ * ones three times.  Written ranges, from a tensor's first element to its last with
+ * what lies between its rows, overlap nothing else (CC_ERR_ALIAS).  One launch;
+ * allocates nothing.
  */
 CC_API int cc_layernorm_forward(const void *x, size_t ldx, const void *residual, size_t ldr,
                                 const void *weight, const void *bias, void *y, size_t ldy,
@@ -734,9 +736,11 @@ CC_API int cc_layernorm_forward(const void *x, size_t ldx, const void *residual,
  *                  cc_layernorm_backward_workspace gives for rows and cols;
  *                  may be NULL when dweight and dbias are.  Calls that share
  *                  one must be ordered.
- *   the rest       as the forward (rows of odd lengths are fast where all
- *                  tensors are contiguous from 16-byte boundaries on).  One
- *                  launch or two; allocates nothing.
+ *   the rest       as the forward.  Rows of odd lengths take up to twice the time
+ *                  where all tensors are contiguous from 16-byte boundaries on.
+ *                  Five to eleven times take: other rows off 16-byte boundaries, more
+ *                  than 16384 columns, and fp32 with dsum from 14081 columns on.
+ *                  One launch or two; allocates nothing.
  */
 CC_API int cc_layernorm_backward(const void *dy, size_t lddy, const void *x, size_t ldx,
                                  const void *weight, const float *mean, const float *rstd,
